@@ -33,6 +33,11 @@ from .ops import (  # noqa: F401
     svdq_act_amax_noalloc,
     svdq_quantize_act_lowrank_down_dyn,
     svdq_w4a4_nvfp4_linear_dyn,
+    LoraPlan,
+    svdq_lora_workspace_bytes,
+    svdq_lora_add,
+    svdq_qk_norm_rope,
+    svdq_rope_axes_tables,
     SvdqW4A4Linear,
     AwqW4A16Linear,
 )

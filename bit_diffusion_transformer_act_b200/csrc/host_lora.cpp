@@ -1,0 +1,161 @@
+// Host side of the per-request adapters: packs a batch's plan (lora_plan.h).  No GPU work.
+
+#include <string.h>
+
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include "../../include/svdq.h"
+#include "lora_plan.h"
+
+namespace {
+
+using svdq::kLoraGroupRows;
+using svdq::kLoraTileRows;
+
+bool sizes_ok(int M, int requests, int slots) {
+  return M >= 0 && requests >= 0 && requests <= (1 << 24) && slots >= 1 && slots <= svdq::kLoraMaxSlots;
+}
+
+size_t tiles_of(size_t rows) { return (rows + kLoraTileRows - 1) / kLoraTileRows; }
+
+// What a plan holds, counted or written (out null: counted only).
+struct Pack {
+  const int32_t* off;
+  const int32_t* ids;
+  const float* w;
+  int requests, slots, M;
+  std::vector<int> shorts;                 // short requests, ordered by their adapter ids
+  size_t tiles = 0, copies = 0, groups = 0;
+
+  bool has_adapter(int r) const {
+    for (int j = 0; j < slots; ++j)
+      if (ids[static_cast<size_t>(r) * slots + j] >= 0) return true;
+    return false;
+  }
+  int rows(int r) const { return off[r + 1] - off[r]; }
+  bool is_short(int r) const { return rows(r) <= svdq::kLoraShortRows; }
+
+  // runs of rows that no adapter touches: f(first row, rows)
+  template <class F>
+  void untouched(F f) const {
+    int from = 0;                          // first row not yet accounted for
+    for (int r = 0; r < requests; ++r) {
+      if (rows(r) == 0 || !has_adapter(r)) continue;
+      if (off[r] > from) f(from, off[r] - from);
+      from = off[r + 1];
+    }
+    if (M > from) f(from, M - from);
+  }
+
+  int compare_ids(int a, int b) const {
+    const int32_t *x = ids + static_cast<size_t>(a) * slots, *y = ids + static_cast<size_t>(b) * slots;
+    for (int j = 0; j < slots; ++j)
+      if (x[j] != y[j]) return x[j] < y[j] ? -1 : 1;
+    return 0;
+  }
+
+  // groups of at most kLoraGroupRows rows of short requests with the same ids, in order:
+  // f(request, row, first of its group)
+  template <class F>
+  void grouped(F f) const {
+    int held = 0;
+    for (size_t i = 0; i < shorts.size(); ++i) {
+      const int r = shorts[i];
+      if (i > 0 && compare_ids(shorts[i - 1], r) != 0) held = 0;
+      for (int m = off[r]; m < off[r + 1]; ++m) {
+        f(r, m, held == 0);
+        held = (held + 1) % kLoraGroupRows;
+      }
+    }
+  }
+
+  void count() {
+    for (int r = 0; r < requests; ++r) {
+      if (rows(r) == 0 || !has_adapter(r)) continue;
+      if (is_short(r)) shorts.push_back(r);
+      else tiles += tiles_of(rows(r));
+    }
+    std::stable_sort(shorts.begin(), shorts.end(), [&](int a, int b) { return compare_ids(a, b) < 0; });
+    untouched([&](int, int n) { copies += tiles_of(n); });
+    grouped([&](int, int, bool first) { groups += first; });
+  }
+
+  void write(int32_t* out, int adapters) const {
+    const svdq::LoraLayout L = svdq::lora_layout(requests, slots, tiles + copies, groups);
+    memset(out, 0, L.words * sizeof(int32_t));
+    memcpy(out, "SVDQLORA", 8);
+    const int32_t head[7] = {M, requests, slots, adapters, static_cast<int32_t>(tiles), static_cast<int32_t>(copies),
+                             static_cast<int32_t>(groups)};
+    memcpy(out + 2, head, sizeof(head));
+    for (int r = 0; r < requests; ++r) {
+      int32_t* q = out + L.requests + static_cast<size_t>(r) * 2 * slots;
+      memcpy(q, ids + static_cast<size_t>(r) * slots, slots * sizeof(int32_t));
+      memcpy(q + slots, w + static_cast<size_t>(r) * slots, slots * sizeof(float));
+    }
+    int32_t* t = out + L.tiles;
+    auto put = [&](int row, int n, int r) {
+      for (; n > 0; row += kLoraTileRows, n -= kLoraTileRows, t += 4) {
+        t[0] = row;
+        t[1] = std::min(n, kLoraTileRows);
+        t[2] = r;
+      }
+    };
+    for (int r = 0; r < requests; ++r)
+      if (rows(r) > 0 && has_adapter(r) && !is_short(r)) put(off[r], rows(r), r);
+    untouched([&](int row, int n) { put(row, n, -1); });
+    int32_t* g = nullptr;
+    int32_t* next = out + L.groups;
+    grouped([&](int r, int m, bool first) {
+      if (first) {
+        g = next;
+        next += svdq::lora_group_words(slots);
+        for (int j = 0; j < 8; ++j) g[4 + j] = j < slots ? ids[static_cast<size_t>(r) * slots + j] : -1;
+      }
+      const int i = g[0]++;
+      g[12 + i] = m;
+      memcpy(g + 12 + kLoraGroupRows + i * slots, w + static_cast<size_t>(r) * slots, slots * sizeof(float));
+    });
+  }
+};
+
+}  // namespace
+
+extern "C" {
+
+size_t svdq_lora_plan_bytes(int M, int requests, int slots) {
+  if (!sizes_ok(M, requests, slots)) return 0;
+  const size_t r = static_cast<size_t>(requests), m = static_cast<size_t>(M);
+  // every request, and every run of rows between requests, ends in a tile or group that may not be full
+  const size_t tiles = 2 * (m / kLoraTileRows + r + 1);
+  const size_t groups = m / kLoraGroupRows + r;
+  return svdq::lora_layout(r, slots, tiles, groups).words * sizeof(int32_t);
+}
+
+int svdq_lora_plan_pack(const int32_t* row_offsets, const int32_t* adapter_ids, const float* weights, int requests,
+                        int slots, int M, int adapters, void* out, size_t out_bytes, svdq_lora_plan* plan) {
+  if (!sizes_ok(M, requests, slots) || adapters < 0 || !out || !plan) return SVDQ_ERR_INVALID_ARG;
+  if (requests > 0 && (!row_offsets || !adapter_ids || !weights)) return SVDQ_ERR_INVALID_ARG;
+  if (requests > 0 && row_offsets[0] < 0) return SVDQ_ERR_INVALID_ARG;
+  for (int r = 0; r < requests; ++r)
+    if (row_offsets[r + 1] < row_offsets[r]) return SVDQ_ERR_INVALID_ARG;
+  if (requests > 0 && row_offsets[requests] > M) return SVDQ_ERR_INVALID_ARG;
+  for (size_t i = 0; i < static_cast<size_t>(requests) * slots; ++i)
+    if (adapter_ids[i] < -1 || adapter_ids[i] >= adapters || !std::isfinite(weights[i])) return SVDQ_ERR_INVALID_ARG;
+  try {
+    Pack p{row_offsets, adapter_ids, weights, requests, slots, M, {}};
+    p.count();
+    const svdq::LoraLayout L = svdq::lora_layout(requests, slots, p.tiles + p.copies, p.groups);
+    if (out_bytes < L.words * sizeof(int32_t)) return SVDQ_ERR_INVALID_ARG;
+    p.write(static_cast<int32_t*>(out), adapters);
+    *plan = svdq_lora_plan{M, requests, slots, adapters, static_cast<int32_t>(p.tiles),
+                           static_cast<int32_t>(p.copies), static_cast<int32_t>(p.groups), 0};
+    plan->bytes = static_cast<int64_t>(L.words * sizeof(int32_t));
+  } catch (...) {                          // no memory for the host's lists
+    return SVDQ_ERR_INVALID_ARG;
+  }
+  return SVDQ_OK;
+}
+
+}  // extern "C"

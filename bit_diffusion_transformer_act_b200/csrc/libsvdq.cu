@@ -22,6 +22,8 @@
 #include "awq_umma.cuh"
 #include "gemm_gelu_quant.cuh"
 #include "gemm_int4.cuh"
+#include "lora_short.cuh"
+#include "rope.cuh"
 
 // Scratch of svdq_act_amax_noalloc: kernel 5's result word, partial maximum and block
 // counter, for callers that cannot allocate device memory.  Every GPU that loads this
@@ -185,6 +187,36 @@ int amax_noalloc_scratch(int dev, unsigned int** out) {
   }
   *out = reinterpret_cast<unsigned int*>(a);
   return SVDQ_OK;
+}
+
+// Two row-strided bf16 matrices (elements (m, c) at ptr[m * ld + c], c < width): whether they may share an
+// element.  Windows of one matrix (equal row strides) are told apart by their columns.
+bool rows_overlap(const void* a, int64_t lda, int64_t wa, const void* b, int64_t ldb, int64_t wb, int64_t rows) {
+  const intptr_t pa = reinterpret_cast<intptr_t>(a) / 2, pb = reinterpret_cast<intptr_t>(b) / 2;
+  if (pa + (rows - 1) * lda + wa <= pb || pb + (rows - 1) * ldb + wb <= pa) return false;
+  if (lda != ldb || wa > lda || wb > lda) return true;
+  const int64_t d = ((pb - pa) % lda + lda) % lda;        // b's first column in a's rows
+  return !(d >= wa && d + wb <= lda);
+}
+
+// Launches `kernel` with programmatic dependent launch.
+template <class... KArgs, class... Args>
+bool launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, int smem, void* stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // see grid_dependency_wait
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return false;
+  }
+  return true;
 }
 
 int launch_status() {
@@ -840,6 +872,282 @@ int awq_w4a16_linear(const void* X, const void* qweight, const void* scales, con
     }
   }
 #undef SVDQ_AWQ_LAUNCH
+  return launch_status();
+}
+
+// CTAs over which a group's K is split in kernel 11: as many as keep the grid within about four CTAs
+// per SM, each with at least 16 steps of 32 K (two per warp).
+static int lora_short_splits(int groups, int K, int jr, int dev) {
+  const int64_t ctas = static_cast<int64_t>(groups) * (jr / 16);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({4 * sm_count(dev) / ctas, K / 512, 16})));
+}
+
+static bool lora_plan_ok(const svdq_lora_plan* p) {
+  return p && p->M >= 0 && p->requests >= 0 && p->slots >= 1 && p->slots <= svdq::kLoraMaxSlots && p->adapters >= 0 &&
+         p->tiles >= 0 && p->copy_tiles >= 0 && p->groups >= 0 &&
+         p->bytes == static_cast<int64_t>(4 * svdq::lora_layout(p->requests, p->slots,
+                                                                static_cast<size_t>(p->tiles) + p->copy_tiles,
+                                                                p->groups).words);
+}
+
+size_t svdq_lora_workspace_bytes(const svdq_lora_plan* plan, int K, int rank) {
+  if (!lora_plan_ok(plan) || K <= 0 || K % 64 != 0 || rank <= 0 || rank % 16 != 0 ||
+      plan->slots * rank > svdq::kLoraMaxRank)
+    return 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  const int jr = plan->slots * rank;
+  size_t bytes = 16;
+  if (plan->groups > 0)
+    bytes += static_cast<size_t>(plan->groups) * lora_short_splits(plan->groups, K, jr, dev) * svdq::kLoraGroupRows *
+             jr * sizeof(float);
+  return bytes;
+}
+
+int svdq_lora_add(const void* X, int64_t ldx, const void* Yin, int64_t ldyin, const void* A, const void* B,
+                  const svdq_lora_plan* plan, const void* plan_dev, size_t plan_bytes, int M, int N, int K, int rank,
+                  void* workspace, size_t workspace_bytes, void* Y, int64_t ldy, void* stream) {
+  if (M < 0 || N <= 0 || K <= 0 || rank <= 0 || !lora_plan_ok(plan) || plan->M != M) return SVDQ_ERR_INVALID_ARG;
+  if (rank % 16 != 0 || plan->slots * static_cast<int64_t>(rank) > svdq::kLoraMaxRank || K % 64 != 0 || N % 64 != 0)
+    return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return SVDQ_OK;
+  if (!Yin || !Y || !aligned16(Yin) || !aligned16(Y) || ldyin < N || ldy < N || ldyin % 8 != 0 || ldy % 8 != 0)
+    return SVDQ_ERR_INVALID_ARG;
+  const bool in_place = Y == Yin && ldy == ldyin;
+  if (!in_place && rows_overlap(Yin, ldyin, N, Y, ldy, N, M)) return SVDQ_ERR_INVALID_ARG;
+  if (!plan_dev || !aligned16(plan_dev) || plan_bytes < static_cast<size_t>(plan->bytes)) return SVDQ_ERR_INVALID_ARG;
+  const bool work = plan->tiles > 0 || plan->groups > 0;
+  if (work) {
+    if (!X || !A || !B || !workspace || !aligned16(X) || !aligned16(A) || !aligned16(B) || !aligned16(workspace) ||
+        ldx < K || ldx % 8 != 0)
+      return SVDQ_ERR_INVALID_ARG;
+    if (rows_overlap(X, ldx, K, Y, ldy, N, M)) return SVDQ_ERR_INVALID_ARG;
+  }
+  int dev;
+  if (int st = current_device_ok(&dev)) return st;
+  if (work && workspace_bytes < svdq_lora_workspace_bytes(plan, K, rank)) return SVDQ_ERR_INVALID_ARG;
+
+  const svdq::LoraLayout L =
+      svdq::lora_layout(plan->requests, plan->slots, static_cast<size_t>(plan->tiles) + plan->copy_tiles, plan->groups);
+  const int32_t* words = static_cast<const int32_t*>(plan_dev);
+  const int jr = plan->slots * rank;
+  namespace k11 = svdq::k11;
+  if (plan->copy_tiles > 0 && !in_place) {
+    const int tiles_n = std::max(1, std::min(16, 4 * sm_count(dev) / plan->copy_tiles));
+    if (!launch_pdl(k11::lora_copy_kernel, dim3(plan->copy_tiles, tiles_n), k11::kThreads, 0, stream,
+                    static_cast<const __nv_bfloat16*>(Yin), static_cast<long long>(ldyin),
+                    static_cast<__nv_bfloat16*>(Y), static_cast<long long>(ldy), N,
+                    words + L.tiles + 4 * static_cast<size_t>(plan->tiles)))
+      return SVDQ_ERR_CUDA;
+  }
+  if (plan->groups > 0) {
+    k11::Params p;
+    p.X = static_cast<const __nv_bfloat16*>(X);
+    p.A = static_cast<const __nv_bfloat16*>(A);
+    p.B = static_cast<const __nv_bfloat16*>(B);
+    p.Yin = static_cast<const __nv_bfloat16*>(Yin);
+    p.Y = static_cast<__nv_bfloat16*>(Y);
+    p.ldx = ldx;
+    p.ldyin = ldyin;
+    p.ldy = ldy;
+    p.groups = words + L.groups;
+    p.part = static_cast<float*>(workspace);
+    p.N = N;
+    p.K = K;
+    p.rank = rank;
+    p.slots = plan->slots;
+    p.ks = lora_short_splits(plan->groups, K, jr, dev);
+    if (!launch_pdl(k11::lora_short_down_kernel, dim3(plan->groups, jr / 16, p.ks), k11::kThreads, 0, stream, p))
+      return SVDQ_ERR_CUDA;
+    const int strips = (N / 16 + k11::kWarps - 1) / k11::kWarps;
+    const int ny = std::max(1, std::min(strips, 8 * sm_count(dev) / plan->groups));
+    if (!launch_pdl(k11::lora_short_up_kernel, dim3(plan->groups, ny), k11::kThreads, 0, stream, p))
+      return SVDQ_ERR_CUDA;
+  }
+  return launch_status();
+}
+
+// The pairs' frequencies in turns per unit of position.  Along an axis they are a geometric sequence; with 64-bit products the last of 128 is off by
+// at most 128 * 2^-53, as far as the position's product itself at 2^7 turns.
+static void rope_freqs(int axes, const int32_t* dims, const double* theta, svdq::k9::Freqs* fr, int* rot) {
+  int at = 0;
+  for (int a = 0; a < axes; ++a) {
+    const double ratio = std::pow(theta[a], -2.0 / dims[a]);
+    double f = 0.15915494309189533577;             // 1 / (2 pi)
+    for (int i = 0; i < dims[a] / 2; ++i, ++at) {
+      fr->f[at] = f;
+      fr->axis[at] = static_cast<uint8_t>(a);
+      f *= ratio;
+    }
+  }
+  *rot = 2 * at;
+  for (; at < svdq::k9::kMaxPairs; ++at) {
+    fr->f[at] = 0.0;
+    fr->axis[at] = 0;
+  }
+}
+
+// Checks of the arguments that both rotary calls share.
+static int rope_check(const void* positions, int P, int axes, const int32_t* dims, const double* theta, int M,
+                      int head_dim) {
+  if (M < 0 || head_dim <= 0 || axes <= 0 || !dims || !theta) return SVDQ_ERR_INVALID_ARG;
+  if (axes > svdq::k9::kMaxAxes || head_dim > 2 * svdq::k9::kMaxPairs) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  int64_t rot = 0;
+  for (int a = 0; a < axes; ++a) {
+    if (dims[a] <= 0 || !(theta[a] > 0.0) || !std::isfinite(theta[a])) return SVDQ_ERR_INVALID_ARG;
+    if (dims[a] % 2 != 0) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    rot += dims[a];
+  }
+  if (rot % 8 != 0 || rot > head_dim) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return SVDQ_OK;
+  if (P <= 0 || M % P != 0) return SVDQ_ERR_INVALID_ARG;
+  if (!positions || !aligned16(positions)) return SVDQ_ERR_INVALID_ARG;
+  return SVDQ_OK;
+}
+
+// A [M, heads, D] view with strides, made canonical where an extent is 1 (its stride then says nothing).
+struct HeadsView {
+  const void* ptr;
+  int64_t row, head;
+  int heads;
+};
+static HeadsView heads_view(const void* ptr, int64_t row, int64_t head, int heads, int M, int D) {
+  if (heads <= 1) head = D;
+  if (M <= 1) row = std::max<int64_t>(D, head * std::max(1, heads - 1) + D);
+  return {ptr, row, head, heads};
+}
+static bool heads_ok(const HeadsView& v) {
+  return v.ptr && aligned16(v.ptr) && v.row >= 0 && v.head >= 0 && v.row % 8 == 0 && v.head % 8 == 0;
+}
+// No two elements of the view are the same word.
+static bool heads_distinct(const HeadsView& v, int M, int D) {
+  const bool by_token = v.head >= D && v.row >= (v.heads - 1) * v.head + D;
+  const bool by_head = v.row >= D && v.head >= (M - 1) * v.row + D;
+  return by_token || by_head || (v.heads == 1 && v.row >= D);
+}
+static bool heads_overlap(const HeadsView& a, const HeadsView& b, int M, int D) {
+  // token-major views are matrices of rows; any other is told apart by its range only
+  const int64_t wa = (a.heads - 1) * a.head + D, wb = (b.heads - 1) * b.head + D;
+  return rows_overlap(a.ptr, a.row, wa, b.ptr, b.row, wb, M);
+}
+
+int svdq_qk_norm_rope(const void* Q, int64_t q_row_stride, int64_t q_head_stride, int q_heads, const void* K,
+                      int64_t k_row_stride, int64_t k_head_stride, int k_heads, int M, int head_dim,
+                      const void* norm_wq, const void* norm_wk, float eps, const void* positions, int positions_float,
+                      int P, int axes, const int32_t* axis_dims, const double* axis_theta, int pairing, void* out_q,
+                      int64_t oq_row_stride, int64_t oq_head_stride, void* out_k, int64_t ok_row_stride,
+                      int64_t ok_head_stride, void* stream) {
+  if (q_heads < 0 || k_heads < 0 || q_heads > (1 << 16) || k_heads > (1 << 16) || (pairing != 0 && pairing != 1))
+    return SVDQ_ERR_INVALID_ARG;
+  if ((norm_wq || norm_wk) && (!(eps >= 0.f) || !std::isfinite(eps))) return SVDQ_ERR_INVALID_ARG;
+  if (int st = rope_check(positions, P, axes, axis_dims, axis_theta, M, head_dim)) return st;
+  const int D = head_dim;
+  if (D % 8 != 0) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0 || q_heads + k_heads == 0) return SVDQ_OK;
+  if ((norm_wq && !aligned16(norm_wq)) || (norm_wk && !aligned16(norm_wk))) return SVDQ_ERR_INVALID_ARG;
+  const HeadsView q = heads_view(Q, q_row_stride, q_head_stride, q_heads, M, D);
+  const HeadsView k = heads_view(K, k_row_stride, k_head_stride, k_heads, M, D);
+  const HeadsView oq = heads_view(out_q, oq_row_stride, oq_head_stride, q_heads, M, D);
+  const HeadsView ok = heads_view(out_k, ok_row_stride, ok_head_stride, k_heads, M, D);
+  auto same = [](const HeadsView& a, const HeadsView& b) { return a.ptr == b.ptr && a.row == b.row && a.head == b.head; };
+  if (q_heads > 0 && (!heads_ok(q) || !heads_ok(oq) || !heads_distinct(oq, M, D) ||
+                      (!same(q, oq) && heads_overlap(q, oq, M, D))))
+    return SVDQ_ERR_INVALID_ARG;
+  if (k_heads > 0 && (!heads_ok(k) || !heads_ok(ok) || !heads_distinct(ok, M, D) ||
+                      (!same(k, ok) && heads_overlap(k, ok, M, D))))
+    return SVDQ_ERR_INVALID_ARG;
+  if (q_heads > 0 && k_heads > 0 &&
+      (heads_overlap(oq, ok, M, D) || heads_overlap(oq, k, M, D) || heads_overlap(ok, q, M, D)))
+    return SVDQ_ERR_INVALID_ARG;
+  int dev;
+  if (int st = current_device_ok(&dev)) return st;
+
+  namespace k9 = svdq::k9;
+  k9::Freqs fr;
+  k9::Params p;
+  rope_freqs(axes, axis_dims, axis_theta, &fr, &p.rot);
+  auto view = [](const HeadsView& v) {
+    return k9::View{static_cast<__nv_bfloat16*>(const_cast<void*>(v.ptr)), v.row, v.head};
+  };
+  p.q = view(q);
+  p.k = view(k);
+  p.oq = view(oq);
+  p.ok = view(ok);
+  p.wq = static_cast<const __nv_bfloat16*>(norm_wq);
+  p.wk = static_cast<const __nv_bfloat16*>(norm_wk);
+  p.pos = positions;
+  p.pos_float = positions_float != 0;
+  p.axes = axes;
+  p.P = P;
+  p.M = M;
+  p.q_heads = q_heads;
+  p.heads = q_heads + k_heads;
+  p.D = D;
+  p.eps = eps;
+  // 8 pairs per lane where runs of 8 fit the head and the rotated columns, else 4
+  const int V = D % 16 == 0 && p.rot % 16 == 0 ? 8 : 4;
+  int lpr = 1;
+  while (lpr * 2 * V < D) lpr *= 2;
+  // warps per token: as many as the token's heads can use while the grid has fewer than 16 per SM
+  const int passes = (p.heads + 32 / lpr - 1) / (32 / lpr);
+  const int64_t most = 16ll * sm_count(dev);
+  p.parts = 1;
+  while (p.parts < 8 && 2 * p.parts <= passes && M * 2ll * p.parts <= most) p.parts *= 2;
+  const int64_t blocks = (static_cast<int64_t>(M) * p.parts + k9::kThreads / 32 - 1) / (k9::kThreads / 32);
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(blocks, 4ll * sm_count(dev))));
+#define SVDQ_ROPE_CASE(V_, L_)                                                                                  \
+  if (V == V_ && lpr == L_)                                                                                     \
+    return launch_pdl(pairing ? k9::qk_norm_rope_kernel<V_, L_, true> : k9::qk_norm_rope_kernel<V_, L_, false>, \
+                      grid, k9::kThreads, 0, stream, p, fr)                                                     \
+               ? launch_status()                                                                                \
+               : SVDQ_ERR_CUDA
+  SVDQ_ROPE_CASE(8, 1);
+  SVDQ_ROPE_CASE(8, 2);
+  SVDQ_ROPE_CASE(8, 4);
+  SVDQ_ROPE_CASE(8, 8);
+  SVDQ_ROPE_CASE(8, 16);
+  SVDQ_ROPE_CASE(4, 1);
+  SVDQ_ROPE_CASE(4, 2);
+  SVDQ_ROPE_CASE(4, 4);
+  SVDQ_ROPE_CASE(4, 8);
+  SVDQ_ROPE_CASE(4, 16);
+  SVDQ_ROPE_CASE(4, 32);
+#undef SVDQ_ROPE_CASE
+  return SVDQ_ERR_UNSUPPORTED_SHAPE;
+}
+
+int svdq_rope_axes_tables(const void* positions, int positions_float, int P, int axes, const int32_t* axis_dims,
+                          const double* axis_theta, int M, int head_dim, void* rope_cos, void* rope_sin,
+                          void* stream) {
+  if (int st = rope_check(positions, P, axes, axis_dims, axis_theta, M, head_dim)) return st;
+  if (head_dim % 2 != 0) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return SVDQ_OK;
+  if (!rope_cos || !rope_sin || !aligned16(rope_cos) || !aligned16(rope_sin)) return SVDQ_ERR_INVALID_ARG;
+  int dev;
+  if (int st = current_device_ok(&dev)) return st;
+  namespace k9 = svdq::k9;
+  k9::Freqs fr;
+  k9::TableParams p;
+  int rot = 0;
+  rope_freqs(axes, axis_dims, axis_theta, &fr, &rot);
+  p.pos = positions;
+  p.pos_float = positions_float != 0;
+  p.axes = axes;
+  p.P = P;
+  p.M = M;
+  p.pairs = head_dim / 2;
+  p.rot_pairs = rot / 2;
+  p.cos = static_cast<float*>(rope_cos);
+  p.sin = static_cast<float*>(rope_sin);
+  const int bx = (P + k9::kThreads - 1) / k9::kThreads;
+  // pairs per thread: the fewest that keep the grid within eight blocks per SM
+  const int by = std::max(1, std::min(p.pairs, 8 * sm_count(dev) / bx));
+  p.per = (p.pairs + by - 1) / by;
+  if (!launch_pdl(k9::rope_tables_kernel, dim3(bx, (p.pairs + p.per - 1) / p.per), k9::kThreads, 0, stream, p, fr))
+    return SVDQ_ERR_CUDA;
   return launch_status();
 }
 

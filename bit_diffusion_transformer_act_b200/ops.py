@@ -26,11 +26,17 @@ class SvdqError(RuntimeError):
         super().__init__(f"{fn} failed: {_STATUS.get(status, 'unknown')} (status {status})")
 
 
+class LoraPlanStruct(ctypes.Structure):
+    """svdq_lora_plan of the header: the sizes of a packed plan."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "requests", "slots", "adapters", "tiles", "copy_tiles", "groups",
+                                              "reserved")] + [("bytes", ctypes.c_int64)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libsvdq.so not built at {LIB_PATH}; run `python bit_diffusion_transformer_act_b200/build.py`")
     lib = ctypes.CDLL(LIB_PATH)
-    vp, i, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    vp, i, f, sz, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_int64
     sig = {
         "svdq_status_string": ([i], ctypes.c_char_p),
         "svdq_abi_version": ([], i),
@@ -58,6 +64,13 @@ def _load():
         "svdq_swizzle_scales": ([vp, i, i, vp], i),
         "svdq_device_status": ([i], i),
         "svdq_selftest_wait_timeout": ([vp], i),
+        "svdq_lora_plan_bytes": ([i, i, i], sz),
+        "svdq_lora_plan_pack": ([vp, vp, vp, i, i, i, i, vp, sz, vp], i),
+        "svdq_lora_workspace_bytes": ([vp, i, i], sz),
+        "svdq_lora_add": ([vp, i64, vp, i64, vp, vp, vp, vp, sz, i, i, i, i, vp, sz, vp, i64, vp], i),
+        "svdq_qk_norm_rope": ([vp, i64, i64, i, vp, i64, i64, i, i, i, vp, vp, f, vp, i, i, i, vp, vp, i, vp, i64, i64,
+                               vp, i64, i64, vp], i),
+        "svdq_rope_axes_tables": ([vp, i, i, i, vp, vp, i, i, vp, vp, vp], i),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -74,7 +87,9 @@ EXPORTED = ("svdq_status_string", "svdq_abi_version", "svdq_packed_weight_bytes"
             "svdq_act_amax_noalloc", "svdq_w4a4_nvfp4_linear_qkv", "svdq_gelu_quant_workspace_bytes",
             "svdq_w4a4_nvfp4_linear_gelu_quant", "svdq_selftest_wait_timeout", "svdq_gelu_table_bytes",
             "svdq_gelu_table_fill", "svdq_int4_packed_weight_bytes", "svdq_int4_pack_weights",
-            "svdq_int4_quantize_act_lowrank_down", "svdq_w4a4_int4_linear")
+            "svdq_int4_quantize_act_lowrank_down", "svdq_w4a4_int4_linear", "svdq_lora_plan_bytes",
+            "svdq_lora_plan_pack", "svdq_lora_workspace_bytes", "svdq_lora_add", "svdq_qk_norm_rope",
+            "svdq_rope_axes_tables")
 
 
 def _check(fn, st):
@@ -491,6 +506,191 @@ def awq_w4a16_linear(X, qweight, scales, zeros, bias=None, Y=None):
                               _ptr(Y), _stream())
     _check("awq_w4a16_linear", st)
     return Y
+
+
+def _int32_array(v, name):
+    a = np.asarray(v)
+    if a.size and (a.dtype.kind not in "iu" or a.min() < -(2 ** 31) or a.max() >= 2 ** 31):
+        raise ValueError(f"{name}: 32-bit integers expected")
+    return np.ascontiguousarray(a, dtype=np.int32)
+
+
+class LoraPlan:
+    """The plan of a batch whose requests carry low-rank adapters (svdq_lora_plan_pack): which rows belong
+    to which request, which adapters each has, and how strongly.  One plan serves every layer and
+    step of the batch.
+
+    row_offsets [requests + 1] (host integers): request s owns rows row_offsets[s] .. row_offsets[s + 1] - 1
+    of the `rows` rows; adapter_ids [requests, slots] (or [requests]), -1 for none; weights the same shape;
+    adapters: how many the pool holds.  The plan is uploaded on the current stream."""
+
+    def __init__(self, row_offsets, adapter_ids, weights, rows, adapters, device="cuda"):
+        off = _int32_array(row_offsets, "row_offsets").reshape(-1)
+        ids = _int32_array(adapter_ids, "adapter_ids")
+        w = np.ascontiguousarray(weights, dtype=np.float32)
+        if ids.ndim == 1:
+            ids, w = ids[:, None], w.reshape(ids.shape[0], -1)
+        if ids.ndim != 2 or ids.shape != w.shape or off.shape[0] != ids.shape[0] + 1:
+            raise ValueError("row_offsets must be [requests + 1], adapter_ids and weights [requests, slots]")
+        self.rows, self.adapters = int(rows), int(adapters)
+        self.requests, self.slots = ids.shape
+        self.struct = LoraPlanStruct()
+        nbytes = int(LIB.svdq_lora_plan_bytes(self.rows, self.requests, self.slots))
+        if nbytes == 0:
+            _check("svdq_lora_plan_pack", 2)
+        host = np.zeros(nbytes, dtype=np.uint8)
+        _check("svdq_lora_plan_pack",
+               LIB.svdq_lora_plan_pack(_np_ptr(off), _np_ptr(ids), _np_ptr(w), self.requests, self.slots, self.rows,
+                                       self.adapters, _np_ptr(host), nbytes, ctypes.byref(self.struct)))
+        self.words = torch.from_numpy(host[: self.struct.bytes]).to(device)
+
+    @classmethod
+    def from_parts(cls, words, sizes):
+        """The plan of a packed blob on the device and its struct's fields (`sizes()`)."""
+        self = cls.__new__(cls)
+        self.struct = LoraPlanStruct(*sizes)
+        self.words = words
+        self.rows, self.requests = self.struct.M, self.struct.requests
+        self.slots, self.adapters = self.struct.slots, self.struct.adapters
+        return self
+
+    def sizes(self):
+        return [getattr(self.struct, n) for n, _ in LoraPlanStruct._fields_]
+
+
+def _row_strided(t, rows, cols, name):
+    """A bf16 [rows, cols] CUDA tensor whose rows may be apart (a column window of a wider one); its row
+    stride."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name}: expected a torch.bfloat16 tensor of shape {(rows, cols)}, got "
+                         f"{getattr(t, 'dtype', type(t))} {tuple(getattr(t, 'shape', ()))}")
+    ld = t.stride(0) if rows > 1 else max(cols, t.stride(0))
+    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap")
+    _on_device(t, name)
+    return ld
+
+
+def svdq_lora_workspace_bytes(plan, K, rank):
+    return int(LIB.svdq_lora_workspace_bytes(ctypes.byref(plan.struct), K, rank))
+
+
+def svdq_lora_add(X, Y, A, B, plan, out=None, workspace=None):
+    """Y + the adapters of each request: out[m] = Y[m] + sum_j w[s, j] B[id] (A[id] X[m]) for the rows m of
+    request s of `plan` (a LoraPlan); rows without an adapter keep Y.
+
+    X bf16 [M, K], Y bf16 [M, N] (a projection's output for X), rows possibly strided; A bf16
+    [adapters, rank, K], B bf16 [adapters, N, rank].  out: Y itself for in place, a [M, N] tensor that
+    overlaps neither, or None for a new one.  Returns out."""
+    if not isinstance(plan, LoraPlan):
+        raise ValueError("plan must be a LoraPlan")
+    M, K = X.shape
+    adapters, rank, _ = A.shape
+    N = Y.shape[1]
+    if M != plan.rows or adapters != plan.adapters:
+        raise ValueError(f"the plan is for {plan.rows} rows and {plan.adapters} adapters, got {M} and {adapters}")
+    ldx = _row_strided(X, M, K, "X")
+    ldyin = _row_strided(Y, M, N, "Y")
+    _require(A, torch.bfloat16, (adapters, rank, K), "A")
+    _require(B, torch.bfloat16, (adapters, N, rank), "B")
+    _require_blob(plan.words, "plan", plan.struct.bytes)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=Y.device)
+    ldy = _row_strided(out, M, N, "out")
+    ws_bytes = svdq_lora_workspace_bytes(plan, K, rank)
+    if workspace is None:
+        workspace = torch.empty((ws_bytes,), dtype=torch.uint8, device=Y.device)
+    _require_blob(workspace, "workspace", ws_bytes)
+    st = LIB.svdq_lora_add(_ptr(X), ldx, _ptr(Y), ldyin, _ptr(A), _ptr(B), ctypes.byref(plan.struct), _ptr(plan.words),
+                           plan.words.numel(), M, N, K, rank, _ptr(workspace), workspace.numel(), _ptr(out), ldy,
+                           _stream())
+    _check("svdq_lora_add", st)
+    return out
+
+
+def _rope_axes(positions, axes_dims, theta):
+    """Checked positions and the ctypes arrays of the axes: (P, axes, is_float, dims, thetas)."""
+    if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.float32) or \
+            positions.dim() != 2 or not positions.is_contiguous():
+        raise ValueError("positions: expected a contiguous int32 or float32 tensor [P, axes]")
+    _on_device(positions, "positions")
+    P, axes = positions.shape
+    thetas = [theta] * axes if isinstance(theta, (int, float)) else list(theta)
+    if len(axes_dims) != axes or len(thetas) != axes:
+        raise ValueError(f"{axes} axes need {axes} widths and one theta or {axes}")
+    return (P, axes, int(positions.dtype == torch.float32), (ctypes.c_int32 * axes)(*axes_dims),
+            (ctypes.c_double * axes)(*thetas))
+
+
+_PAIRINGS = {"interleaved": 0, "half": 1}
+
+
+def _heads(t, M, D, name):
+    """A bf16 [M, heads, D] CUDA tensor with any strides over tokens and heads."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != M or \
+            t.shape[2] != D:
+        raise ValueError(f"{name}: expected a torch.bfloat16 tensor [{M}, heads, {D}], got "
+                         f"{getattr(t, 'dtype', type(t))} {tuple(getattr(t, 'shape', ()))}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    _on_device(t, name)
+    return t.shape[1], t.stride(0), t.stride(1)
+
+
+def svdq_qk_norm_rope(q, k, norm_wq, norm_wk, eps, positions, axes_dims, theta, pairing="interleaved", out_q=None,
+                      out_k=None):
+    """Per-head RMSNorm and rotary positions with several axes: q bf16 [M, q_heads, D] and k bf16
+    [M, k_heads, D] (or None), with any strides over tokens and heads (views of a packed projection),
+    norm_wq / norm_wk bf16 [D] or None for no normalisation, positions int32 or float32 [P, axes]
+    (token m has position m % P), axes_dims the rotated columns of each axis, theta one value or one per axis,
+    pairing "interleaved" or "half".  out_q / out_k: q / k themselves for in place, tensors of their
+    shape, or None for new ones.  Returns (out_q, out_k)."""
+    M, _, D = (q if q is not None else k).shape
+    P, axes, is_float, dims, thetas = _rope_axes(positions, axes_dims, theta)
+    if pairing not in _PAIRINGS:
+        raise ValueError(f"pairing: one of {sorted(_PAIRINGS)}, got {pairing!r}")
+    args = []
+    outs = []
+    for t, out, w, name in ((q, out_q, norm_wq, "q"), (k, out_k, norm_wk, "k")):
+        if t is None:
+            if out is not None or w is not None:
+                raise ValueError(f"out_{name} and norm_w{name} need {name}")
+            args.append((None, 0, 0, 0, None, 0, 0, None))
+            outs.append(None)
+            continue
+        heads, row, head = _heads(t, M, D, name)
+        if out is None:
+            out = torch.empty((M, heads, D), dtype=torch.bfloat16, device=t.device)
+        oheads, orow, ohead = _heads(out, M, D, "out_" + name)
+        if oheads != heads:
+            raise ValueError(f"out_{name} must have {heads} heads, got {oheads}")
+        if w is not None:
+            _require(w, torch.bfloat16, (D,), "norm_w" + name)
+        args.append((_ptr(t), row, head, heads, _ptr(out), orow, ohead, _ptr(w)))
+        outs.append(out)
+    (qp, qr, qh, nq, oqp, oqr, oqh, wq), (kp, kr, kh, nk, okp, okr, okh, wk) = args
+    st = LIB.svdq_qk_norm_rope(qp, qr, qh, nq, kp, kr, kh, nk, M, D, wq, wk, float(eps), _ptr(positions), is_float, P,
+                               axes, dims, thetas, _PAIRINGS[pairing], oqp, oqr, oqh, okp, okr, okh, _stream())
+    _check("svdq_qk_norm_rope", st)
+    return tuple(outs)
+
+
+def svdq_rope_axes_tables(positions, axes_dims, theta, head_dim, rows=None, rope_cos=None, rope_sin=None):
+    """The (cos, sin) tables, float32 [head_dim / 2, rows], of positions with several axes, in the layout
+    of svdq_w4a4_nvfp4_linear_qkv; arguments as svdq_qk_norm_rope (rows: a multiple of P, by default P)."""
+    P, axes, is_float, dims, thetas = _rope_axes(positions, axes_dims, theta)
+    M = P if rows is None else rows
+    shape = (head_dim // 2, M)
+    if rope_cos is None:
+        rope_cos = torch.empty(shape, dtype=torch.float32, device=positions.device)
+    if rope_sin is None:
+        rope_sin = torch.empty(shape, dtype=torch.float32, device=positions.device)
+    _require(rope_cos, torch.float32, shape, "rope_cos")
+    _require(rope_sin, torch.float32, shape, "rope_sin")
+    st = LIB.svdq_rope_axes_tables(_ptr(positions), is_float, P, axes, dims, thetas, M, head_dim, _ptr(rope_cos),
+                                   _ptr(rope_sin), _stream())
+    _check("svdq_rope_axes_tables", st)
+    return rope_cos, rope_sin
 
 
 # ---------------------------------------------------------------- layers

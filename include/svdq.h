@@ -330,6 +330,89 @@ int awq_w4a16_linear(const void* X, const void* qweight, const void* scales,
                      const void* zeros, const void* bias, int M, int N, int K,
                      void* Y, void* stream);
 
+/* ------------------------------------------------- adapters of many requests */
+
+/* Low-rank adapters beside a shared projection: the projection's 4-bit weights are shared by every
+ * request of a batch, so an adapter cannot be merged into them; it is added to the output,
+ *     Y[m] = Yin[m] + sum_j w[s, j] B[id(s, j)] (A[id(s, j)] X[m])      for every row m of request s,
+ * with Yin the output of any of the linear calls of this header for the same X (or a column window of
+ * it).  A and B hold a pool of adapters in nn.Linear layout, padded to one rank.
+ *
+ * svdq_lora_plan_pack (host): row_offsets int32 [requests + 1], non-decreasing within 0..M: request s
+ *   owns rows row_offsets[s] .. row_offsets[s + 1] - 1 (it may own none); adapter_ids int32
+ *   [requests, slots], -1 for an empty slot; weights float32 [requests, slots], finite (a request's
+ *   strength times the adapter's alpha / r).  Writes the batch's plan to `out` (host, at least
+ *   svdq_lora_plan_bytes(M, requests, slots) bytes; plan->bytes of them are used; device-private
+ *   layout) and its sizes to *plan.  1 <= slots <= 8; requests <= 2^24.  One plan serves every layer and
+ *   step of the batch: copy `out` to the device once.
+ * svdq_lora_add:
+ *   X device bf16 [M, K], Yin and Y device bf16 [M, N], rows ldx, ldyin, ldy elements apart (multiples
+ *     of 8, at least the width); Y is Yin itself (in place: rows that no adapter touches are neither
+ *     read nor written) or overlaps neither Yin nor X (then those rows are copied from Yin)
+ *   A device bf16 [adapters, rank, K], B device bf16 [adapters, N, rank]; a smaller adapter is padded
+ *     with zero ranks
+ *   plan, plan_dev  the host struct and the device copy of the packed plan (plan_bytes of it, at least
+ *     plan->bytes).  Replays of a captured call read plan_dev again: it may be overwritten, in
+ *     stream order, by another plan whose struct is the same.
+ *   workspace  device scratch of at least svdq_lora_workspace_bytes(plan, K, rank) bytes, 16-byte
+ *     aligned (contents need no initialisation; calls that may overlap need one each)
+ *   K % 64 == 0, N % 64 == 0, rank % 16 == 0, slots * rank <= 128; X, Yin, Y, A, B, plan_dev 16-byte aligned.
+ * Arithmetic: products of bf16 values accumulated in fp32; A X enters the second product as a high and
+ * a low bf16 part (2^-16 relative), Y is rounded once.  Repeat calls are bit-identical.
+ * Errors and asynchrony as svdq_w4a4_nvfp4_linear. */
+typedef struct {
+  int32_t M, requests, slots, adapters;
+  int32_t tiles, copy_tiles, groups, reserved;
+  int64_t bytes;
+} svdq_lora_plan;
+
+size_t svdq_lora_plan_bytes(int M, int requests, int slots);    /* 0 for unsupported sizes */
+int svdq_lora_plan_pack(const int32_t* row_offsets, const int32_t* adapter_ids, const float* weights, int requests,
+                        int slots, int M, int adapters, void* out, size_t out_bytes, svdq_lora_plan* plan);
+size_t svdq_lora_workspace_bytes(const svdq_lora_plan* plan, int K, int rank);  /* for the current device */
+int svdq_lora_add(const void* X, int64_t ldx, const void* Yin, int64_t ldyin, const void* A, const void* B,
+                  const svdq_lora_plan* plan, const void* plan_dev, size_t plan_bytes, int M, int N, int K, int rank,
+                  void* workspace, size_t workspace_bytes, void* Y, int64_t ldy, void* stream);
+
+/* ------------------------------------------------- rotary positions with several axes */
+
+/* Rotary positions of images and video: a token has a position on each of `axes` axes (time,
+ * height, width, ...; 1 to 8); axis a turns axis_dims[a] / 2 pairs of a head (axis_dims[a] even, > 0), the
+ * axes' pairs following each other, pair i of axis a by the angle
+ *     positions[m, a] * axis_theta[a]^(-2 i / axis_dims[a]).
+ * The rotated width, the sum of axis_dims, is a multiple of 8 and at most head_dim; the columns after
+ * it are not rotated.  positions: device int32 or (positions_float != 0) float32 [P, axes], any sign;
+ * M % P == 0 and token m has position m % P, so that the images of a batch may share them.
+ * axis_theta > 0, finite.  The angle is formed in 64 bits and reduced to a turn before its sine and
+ * cosine are taken in 32.
+ *
+ * svdq_qk_norm_rope (kernel 9): q and k of a projection RMS-normalised per head and rotated -- what
+ * svdq_w4a4_nvfp4_linear_qkv does in its epilogue, for the layers and shapes that it does not take (a
+ * projection with adapters, whose sum comes before the norm; the int4 and AWQ layers; other head widths,
+ * grouped heads).  x / sqrt(mean(x^2) + eps) * w, then the rotation, in fp32, rounded once.
+ *   Q, K  device bf16: element (m, h, d) at [m * row_stride + h * head_stride + d] (strides in elements,
+ *     multiples of 8), so the thirds of a packed projection, [M, heads, D] and [heads, M, D] are all
+ *     taken as they are; out_q, out_k the same, with strides of their own.  q_heads or k_heads may
+ *     be 0 (its pointers are then not used).
+ *   norm_wq, norm_wk  device bf16 [head_dim], or NULL: no normalisation of q or k (eps is then not used)
+ *   pairing 0: pair i is (x[2 i], x[2 i + 1]) (as svdq_w4a4_nvfp4_linear_qkv); 1: (x[i], x[i + rotated / 2])
+ *   out_q may be Q with Q's strides (in place), likewise out_k; an output overlaps nothing else.
+ * head_dim % 8 == 0, 8..256; every pointer 16-byte aligned.
+ *
+ * svdq_rope_axes_tables (kernel 10): the cos / sin tables of the same positions in the layout that
+ * svdq_w4a4_nvfp4_linear_qkv reads: float32 [head_dim / 2, M], pair-major; pairs past the rotated width
+ * get 1 and 0.  head_dim even, 2..256.
+ * Errors and asynchrony as svdq_w4a4_nvfp4_linear. */
+int svdq_qk_norm_rope(const void* Q, int64_t q_row_stride, int64_t q_head_stride, int q_heads, const void* K,
+                      int64_t k_row_stride, int64_t k_head_stride, int k_heads, int M, int head_dim,
+                      const void* norm_wq, const void* norm_wk, float eps, const void* positions, int positions_float,
+                      int P, int axes, const int32_t* axis_dims, const double* axis_theta, int pairing, void* out_q,
+                      int64_t oq_row_stride, int64_t oq_head_stride, void* out_k, int64_t ok_row_stride,
+                      int64_t ok_head_stride, void* stream);
+int svdq_rope_axes_tables(const void* positions, int positions_float, int P, int axes, const int32_t* axis_dims,
+                          const double* axis_theta, int M, int head_dim, void* rope_cos, void* rope_sin,
+                          void* stream);
+
 /* ----------------------------------------------------------------- helpers */
 
 /* Host: convert a swizzled scale buffer (rows rounded up to 128) into plain

@@ -20,6 +20,8 @@ Everything is plain NumPy in float64, written from the definitions:
   the definition a fused epilogue kernel is to match.
 * ``mlp_epilogue``  the MLP up-projection's epilogue: GELU of the stored output, then the
   down projection's activation pass (NVFP4 codes, scales, low-rank U) on the hidden state.
+* ``adapters``   low-rank adapters of many requests added to a projection's output.
+* ``rope_axes``  rotary positions with several axes, applied to normalised heads, and their tables.
 
 Sources: "Nunchaku Lite" (Hugging Face Diffusers documentation), section
 "Supported quantization types" (method table: svdq_w4a4 / nvfp4 / group 16,

@@ -1,0 +1,193 @@
+"""Per-request low-rank adapters on the GPU against the float64 oracle: every kind of request (a row,
+a few, many; none; no adapter; the same adapter in two slots), strided and in-place outputs, graphs,
+streams, and a run through the layers."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import adapters as oracle
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def P(cuda_lib):
+    return cuda_lib
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _make(M, K, N, R, slots, adapters, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def normal(*shape, scale=1.0):
+        return (torch.randn(shape, generator=g, device="cuda") * scale).to(torch.bfloat16)
+
+    return (normal(M, K), normal(M, N), normal(adapters, R, K, scale=K ** -0.5),
+            normal(adapters, N, R, scale=R ** -0.5))
+
+
+def _weights(ids, seed=0):
+    return np.random.default_rng(seed).uniform(-1.5, 1.5, np.shape(ids)).astype(np.float32)
+
+
+def _check(out, x, y, a, b, off, ids, w):
+    ref, us, ks = oracle.forward(_np(x), _np(y), _np(a), _np(b), off, ids, w)
+    tol = oracle.bound(ref, us, ks, x.shape[1], a.shape[1] * np.shape(ids)[1])
+    bad = ~(np.abs(_np(out) - ref) <= tol)
+    assert not bad.any(), (np.argwhere(bad)[:5], np.max(np.abs(_np(out) - ref) / tol))
+
+
+# M, K, N, rank, slots, adapters, row offsets
+CASES = [
+    (1, 64, 64, 16, 1, 1, [0, 1]),
+    (1, 320, 192, 48, 2, 3, [0, 1]),
+    (2, 2560, 1024, 128, 1, 2, [0, 1, 2]),
+    (9, 128, 128, 32, 1, 4, [0, 9]),
+    (16, 576, 320, 16, 8, 5, [0, 16]),
+    (17, 512, 256, 64, 2, 2, [0, 17]),
+    (40, 256, 64, 16, 3, 3, list(range(41))),                       # a row per request
+    (64, 1024, 448, 32, 4, 2, [0] + list(range(20, 65))),
+    (127, 192, 64, 112, 1, 2, [0, 127]),
+    (128, 64, 128, 32, 2, 2, [0, 128]),
+    (129, 128, 192, 64, 1, 2, [0, 129]),
+    (300, 448, 704, 80, 1, 3, [0, 0, 31, 31, 64, 200, 200, 298]),   # empty requests, rows behind the last
+    (515, 640, 128, 48, 2, 6, [3, 20, 21, 150, 153, 400, 515]),     # rows before the first
+    (700, 2560, 256, 128, 1, 2, [0, 260, 520, 690]),
+    (1300, 128, 2560, 16, 1, 4, [0, 1000, 1001, 1290]),
+]
+
+
+def _ids(case):
+    M, K, N, R, slots, adapters, off = case
+    n = len(off) - 1
+    ids = (np.arange(n * slots).reshape(n, slots) * 7 + 1) % adapters
+    ids[2::3, 0] = -1
+    if slots > 1:
+        ids[1::4, 1] = ids[1::4, 0]                                 # the same adapter twice, or none twice
+    return ids
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(v) for v in c[:6]))
+def test_matches_the_oracle(P, case):
+    M, K, N, R, slots, adapters, off = case
+    x, y, a, b = _make(M, K, N, R, slots, adapters)
+    ids = _ids(case)
+    w = _weights(ids)
+    plan = P.LoraPlan(off, ids, w, M, adapters)
+    before = y.clone()
+    out = P.svdq_lora_add(x, y, a, b, plan)
+    _check(out, x, y, a, b, off, ids, w)
+    assert torch.equal(y, before)
+    assert torch.equal(out, P.svdq_lora_add(x, y, a, b, plan)), "repeat calls are bit-identical"
+    in_place = y.clone()
+    assert P.svdq_lora_add(x, in_place, a, b, plan, out=in_place) is in_place
+    assert torch.equal(in_place, out)
+    assert P.svdq_device_status() == 0
+
+
+@pytest.mark.parametrize("case", [CASES[1], CASES[6], CASES[11], CASES[12]], ids=lambda c: str(c[0]))
+def test_strided_rows_and_column_windows(P, case):
+    M, K, N, R, slots, adapters, off = case
+    x, y, a, b = _make(M, K, N, R, slots, adapters, seed=3)
+    ids = _ids(case)
+    w = _weights(ids)
+    plan = P.LoraPlan(off, ids, w, M, adapters)
+    wide_x = torch.full((M, K + 24), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide_x[:, 8:8 + K] = x
+    wide = torch.full((M, 3 * N + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    wide[:, N:2 * N] = y
+    expect = P.svdq_lora_add(x, y, a, b, plan)
+    # in place on the middle third of a packed projection
+    P.svdq_lora_add(wide_x[:, 8:8 + K], wide[:, N:2 * N], a, b, plan, out=wide[:, N:2 * N])
+    assert torch.equal(wide[:, N:2 * N], expect)
+    assert (wide[:, :N] == 7).all() and (wide[:, 2 * N:] == 7).all()
+    # from one window into another of the same buffer
+    wide[:, N:2 * N] = y
+    P.svdq_lora_add(x, wide[:, N:2 * N], a, b, plan, out=wide[:, 2 * N:3 * N])
+    assert torch.equal(wide[:, 2 * N:3 * N], expect) and torch.equal(wide[:, N:2 * N], y)
+    assert (wide[:, :N] == 7).all() and (wide[:, 3 * N:] == 7).all()
+
+
+def test_untouched_rows_keep_their_bits(P):
+    """In place, rows of no request and of no adapter are left as they were, NaN payloads included;
+    out of place they are copied."""
+    M, K, N = 260, 128, 192
+    x, y, a, b = _make(M, K, N, 16, 1, 2)
+    off, ids = [2, 4, 140, 250], np.array([[0], [-1], [1]])
+    keep = [0, 1] + list(range(4, 140)) + list(range(250, 260))
+    y[keep] = torch.randint(-32768, 32767, (len(keep), N), dtype=torch.int16, device="cuda").view(torch.bfloat16)
+    x[keep] = float("nan")
+    plan = P.LoraPlan(off, ids, np.ones((3, 1)), M, 2)
+    for out in (y.clone(), None):
+        src = y if out is None else out
+        got = P.svdq_lora_add(x, src, a, b, plan, out=out)
+        assert torch.equal(got.view(torch.int16)[keep], y.view(torch.int16)[keep])
+        touched = [i for i in range(M) if i not in keep]
+        assert torch.isfinite(got[touched].float()).all()
+
+
+@pytest.mark.parametrize("rows", [[0, 5, 9], [0, 140, 300]])
+def test_a_bad_row_stays_alone(P, rows):
+    """NaN and infinity in a row of X reach that row only; an empty slot does not turn them into NaN."""
+    M, K, N = rows[-1], 192, 128
+    x, y, a, b = _make(M, K, N, 32, 2, 3)
+    ids = np.array([[-1, -1], [0, -1]])
+    w = np.ones((2, 2), np.float32)
+    x[1] = float("inf")
+    x[rows[1] + 1] = float("nan")
+    got = P.svdq_lora_add(x, y, a, b, P.LoraPlan(rows, ids, w, M, 3))
+    assert torch.equal(got[: rows[1]], y[: rows[1]])
+    bad = torch.isnan(got.float()).any(1).nonzero().flatten().tolist()
+    assert bad == [rows[1] + 1]
+    ids = np.array([[-1, 1], [0, 2]])
+    x[1] = 1.0
+    got = P.svdq_lora_add(x, y, a, b, P.LoraPlan(rows, ids, w, M, 3))
+    keep = [i for i in range(M) if i != rows[1] + 1]
+    x[rows[1] + 1] = 0.0
+    ref, us, ks = oracle.forward(_np(x), _np(y), _np(a), _np(b), rows, ids, w)
+    assert (np.abs(_np(got) - ref) <= oracle.bound(ref, us, ks, K, 64))[keep].all()
+
+
+def test_graph_replays_read_the_plan_again(P):
+    M, K, N = 150, 256, 192
+    x, y, a, b = _make(M, K, N, 32, 1, 4)
+    off = [0, 1, 3, 140]
+    w = _weights([[0], [0], [0]])
+    ids1, ids2 = np.array([[0], [1], [2]]), np.array([[3], [2], [0]])
+    p1, p2 = P.LoraPlan(off, ids1, w, M, 4), P.LoraPlan(off, ids2, -w, M, 4)
+    assert p1.sizes() == p2.sizes()
+    out = torch.empty_like(y)
+    P.svdq_lora_add(x, y, a, b, p1, out=out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        P.svdq_lora_add(x, y, a, b, p1, out=out)
+    out.zero_()
+    graph.replay()
+    _check(out, x, y, a, b, off, ids1, w)
+    p1.words.copy_(p2.words)
+    x.mul_(0.5)
+    graph.replay()
+    _check(out, x, y, a, b, off, ids2, -w)
+
+
+def test_two_streams_at_once(P):
+    sets = []
+    for i, (M, off) in enumerate([(600, [0, 1, 300, 600]), (48, list(range(49)))]):
+        x, y, a, b = _make(M, 512, 512, 64, 1, 3, seed=i)
+        ids = np.arange(len(off) - 1)[:, None] % 3
+        w = _weights(ids)
+        sets.append((x, y, a, b, off, ids, w, P.LoraPlan(off, ids, w, M, 3), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(8):
+        for i, (x, y, a, b, off, ids, w, plan, stream) in enumerate(sets):
+            with torch.cuda.stream(stream):
+                outs[i].append(P.svdq_lora_add(x, y, a, b, plan))
+    torch.cuda.synchronize()
+    for i, (x, y, a, b, off, ids, w, plan, _) in enumerate(sets):
+        _check(outs[i][0], x, y, a, b, off, ids, w)
+        assert all(torch.equal(o, outs[i][0]) for o in outs[i])

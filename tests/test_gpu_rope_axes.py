@@ -1,0 +1,131 @@
+"""Rotary positions with several axes on the GPU: the norm-and-rotate call and the tables against the
+float64 oracle, strided and in-place heads, far and fractional positions, and the fused projection fed
+with the tables."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import rope_axes as oracle
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def P(cuda_lib):
+    return cuda_lib
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _positions(P_, axes, fractional, seed):
+    r = np.random.default_rng(seed)
+    pos = r.integers(-200, 70000, size=(P_, axes))
+    pos[0] = 0
+    if fractional:
+        return torch.from_numpy((pos * 0.3125).astype(np.float32)).cuda()
+    return torch.from_numpy(pos.astype(np.int32)).cuda()
+
+
+def _check(got, x, w, eps, pos, dims, thetas, half, M):
+    ang = oracle.angles(_np(pos), dims, thetas)
+    ang = np.tile(ang, (M // ang.shape[0], 1))
+    n = oracle.norm(_np(x), None if w is None else _np(w), eps)
+    ref = oracle.rotate(n, ang, half)
+    tol = oracle.bound(n, ref, half, sum(dims), x.shape[2])
+    bad = ~(np.abs(_np(got) - ref) <= tol)
+    assert not bad.any(), (np.argwhere(bad)[:5], np.max(np.abs(_np(got) - ref) / tol))
+
+
+# M, P, q heads, k heads, D, dims, thetas
+CASES = [
+    (1, 1, 1, 1, 8, [8], [10000.0]),
+    (1, 1, 20, 20, 128, [16, 56, 56], [10000.0] * 3),
+    (3, 3, 5, 3, 128, [44, 42, 42], [10000.0, 100.0, 1e6]),
+    (77, 77, 3, 1, 64, [64], [10000.0]),
+    (50, 25, 4, 4, 96, [24, 36, 36], [256.0] * 3),
+    (33, 11, 2, 7, 80, [16, 32, 32], [10000.0] * 3),
+    (40, 40, 2, 2, 256, [32, 64, 64], [10000.0] * 3),            # 96 columns past the rotated ones
+    (19, 19, 3, 3, 40, [2, 6, 16], [10000.0] * 3),               # runs of four pairs, a tail
+    (21, 21, 1, 2, 248, [120, 128], [500.0, 10000.0]),
+    (12, 12, 2, 1, 16, [2, 2, 2, 2, 2, 2, 2, 2], [3.0, 4.0, 5.0, 6.0, 7.0, 8.0, 9.0, 10.0]),
+    (1025, 1025, 2, 2, 24, [8, 8], [10000.0] * 2),
+]
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(v) for v in c[:5]))
+def test_matches_the_oracle(P, case, half):
+    M, Pn, hq, hk, D, dims, thetas = case
+    g = torch.Generator(device="cuda").manual_seed(1)
+    qkv = torch.randn((M, (hq + 2 * hk) * D), generator=g, device="cuda").to(torch.bfloat16)
+    q, k = qkv[:, : hq * D].view(M, hq, D), qkv[:, hq * D:(hq + hk) * D].view(M, hk, D)
+    wq = torch.randn(D, generator=g, device="cuda").to(torch.bfloat16)
+    wk = torch.randn(D, generator=g, device="cuda").to(torch.bfloat16)
+    pos = _positions(Pn, len(dims), half, 5)
+    keep = qkv.clone()
+    pairing = "half" if half else "interleaved"
+    theta = thetas[0] if len(set(thetas)) == 1 else thetas
+    oq, ok = P.svdq_qk_norm_rope(q, k, wq, wk, 1e-6, pos, dims, theta, pairing)
+    assert torch.equal(qkv, keep)
+    _check(oq, q, wq, 1e-6, pos, dims, thetas, half, M)
+    _check(ok, k, wk, 1e-6, pos, dims, thetas, half, M)
+    # without a norm, and one of the two alone
+    nq, nk = P.svdq_qk_norm_rope(q, k, None, wk, 1e-6, pos, dims, theta, pairing)
+    _check(nq, q, None, 0.0, pos, dims, thetas, half, M)
+    assert torch.equal(nk, ok)
+    only, none = P.svdq_qk_norm_rope(None, k, None, wk, 1e-6, pos, dims, theta, pairing)[::-1]
+    assert none is None and torch.equal(only, ok)
+    # head-major outputs, then in place on the packed projection (v stays)
+    hm = torch.zeros((hq, M, D), dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    P.svdq_qk_norm_rope(q, None, wq, None, 1e-6, pos, dims, theta, pairing, out_q=hm)
+    assert torch.equal(hm, oq)
+    P.svdq_qk_norm_rope(q, k, wq, wk, 1e-6, pos, dims, theta, pairing, out_q=q, out_k=k)
+    assert torch.equal(q, oq) and torch.equal(k, ok)
+    assert torch.equal(qkv[:, (hq + hk) * D:], keep[:, (hq + hk) * D:])
+
+
+@pytest.mark.parametrize("case", CASES + [(4096, 2048, 0, 0, 128, [16, 56, 56], [10000.0] * 3)],
+                         ids=lambda c: "-".join(str(v) for v in c[:5]))
+def test_tables_match_the_oracle(P, case):
+    M, Pn, _, _, D, dims, thetas = case
+    for fractional in (False, True):
+        pos = _positions(Pn, len(dims), fractional, 9)
+        cos, sin = P.svdq_rope_axes_tables(pos, dims, thetas, D, M)
+        assert cos.shape == sin.shape == (D // 2, M)
+        ang = np.tile(oracle.angles(_np(pos), dims, thetas), (M // Pn, 1)).T
+        # the reduced angle's rounding (at most 2^-25 half turns, times pi) and the two ulp of the
+        # sine and cosine; the 64-bit angle by 2^-45 of its size
+        tol = 2.0 ** -22 + np.abs(ang) * 2.0 ** -45
+        n = ang.shape[0]
+        assert (np.abs(_np(cos)[:n] - np.cos(ang)) <= tol).all()
+        assert (np.abs(_np(sin)[:n] - np.sin(ang)) <= tol).all()
+        assert (cos[n:] == 1).all() and (sin[n:] == 0).all()
+
+
+def test_zero_and_infinite_rows(P):
+    """A zero head stays zero (eps under the root); a NaN stays in its head; columns past the rotated
+    ones are not touched by their neighbours."""
+    q = torch.randn((4, 3, 64), device="cuda").to(torch.bfloat16)
+    q[0, 1] = 0
+    q[2, 0, 5] = float("nan")
+    q[3, 2, 40] = float("inf")
+    pos = torch.arange(8, dtype=torch.int32, device="cuda").view(4, 2)
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    out, _ = P.svdq_qk_norm_rope(q, None, w, None, 1e-6, pos, [8, 8], 100.0)
+    assert (out[0, 1] == 0).all()
+    assert torch.isnan(out[2, 0].float()).all() and torch.isfinite(out[2, 1:].float()).all()
+    plain, _ = P.svdq_qk_norm_rope(q, None, None, None, 0.0, pos, [8, 8], 100.0)
+    assert torch.equal(plain[3, 2, 16:], q[3, 2, 16:])
+    assert torch.equal(plain[:, :, 16:].view(torch.int16), q[:, :, 16:].contiguous().view(torch.int16))
+
+
+def test_far_positions_keep_their_angle(P):
+    """Positions near 2^31, where a product in 32 bits has no correct digit left."""
+    pos = torch.tensor([[2 ** 31 - 1], [-(2 ** 31)], [2 ** 30 + 1]], dtype=torch.int32, device="cuda")
+    cos, sin = P.svdq_rope_axes_tables(pos, [64], 10000.0, 64)
+    ang = oracle.angles(_np(pos), [64], [10000.0]).T
+    tol = 2.0 ** -22 + np.abs(ang) * 2.0 ** -45
+    assert (np.abs(_np(cos) - np.cos(ang)) <= tol).all() and (np.abs(_np(sin) - np.sin(ang)) <= tol).all()
