@@ -23,6 +23,7 @@
 #include "gemm_gelu_quant.cuh"
 #include "gemm_int4.cuh"
 #include "lora_short.cuh"
+#include "lora_tile.cuh"
 #include "rope.cuh"
 
 // Scratch of svdq_act_amax_noalloc: kernel 5's result word, partial maximum and block
@@ -88,18 +89,18 @@ EncodeTiledFn encode_fn() {
 // An eager call of the GEMM needs seven maps; encoding them is most of the call's host cost.
 struct TmapKey {
   uintptr_t ptr;
-  uint64_t rows, cols;
+  uint64_t rows, cols, ld;
   uint32_t box_cols, box_rows;
   int dt, elem, sw;
   bool operator==(const TmapKey& o) const {
-    return ptr == o.ptr && rows == o.rows && cols == o.cols && box_cols == o.box_cols && box_rows == o.box_rows &&
+    return ptr == o.ptr && rows == o.rows && cols == o.cols && ld == o.ld && box_cols == o.box_cols && box_rows == o.box_rows &&
            dt == o.dt && elem == o.elem && sw == o.sw;
   }
 };
 struct TmapKeyHash {
   size_t operator()(const TmapKey& k) const {
     uint64_t h = k.ptr * 0x9E3779B97F4A7C15ull;
-    for (uint64_t v : {k.rows, k.cols, static_cast<uint64_t>(k.box_cols) << 32 | k.box_rows,
+    for (uint64_t v : {k.rows, k.cols, k.ld, static_cast<uint64_t>(k.box_cols) << 32 | k.box_rows,
                        static_cast<uint64_t>(k.dt) << 16 | static_cast<uint64_t>(k.elem) << 8 |
                            static_cast<uint64_t>(k.sw)})
       h = (h ^ v) * 0x100000001B3ull;
@@ -108,12 +109,14 @@ struct TmapKeyHash {
 };
 constexpr size_t kTmapCacheMax = 4096;            // cleared when full
 
-// 2-D row-major tensor [rows, cols] of `elem` bytes per element; box {box_cols, box_rows}.
+// 2-D row-major tensor [rows, cols] of `elem` bytes per element, rows `ld` elements apart (0: cols); box
+// {box_cols, box_rows}.
 bool make_tmap(CUtensorMap* m, const void* ptr, CUtensorMapDataType dt, int elem, uint64_t rows, uint64_t cols,
-               uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle sw) {
+               uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle sw, uint64_t ld = 0) {
   static std::mutex mu;
   static std::unordered_map<TmapKey, CUtensorMap, TmapKeyHash> cache;
-  const TmapKey key{reinterpret_cast<uintptr_t>(ptr), rows, cols, box_cols, box_rows, static_cast<int>(dt), elem,
+  if (ld == 0) ld = cols;
+  const TmapKey key{reinterpret_cast<uintptr_t>(ptr), rows, cols, ld, box_cols, box_rows, static_cast<int>(dt), elem,
                     static_cast<int>(sw)};
   {
     std::lock_guard<std::mutex> lock(mu);
@@ -126,7 +129,7 @@ bool make_tmap(CUtensorMap* m, const void* ptr, CUtensorMapDataType dt, int elem
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols * static_cast<uint64_t>(elem)};
+  const cuuint64_t strides[1] = {ld * static_cast<uint64_t>(elem)};
   const cuuint32_t box[2] = {box_cols, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   if (fn(m, dt, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
@@ -199,20 +202,25 @@ bool rows_overlap(const void* a, int64_t lda, int64_t wa, const void* b, int64_t
   return !(d >= wa && d + wb <= lda);
 }
 
-// Launches `kernel` with programmatic dependent launch.
+// Launches `kernel` with programmatic dependent launch, in clusters of cluster_y CTAs along y.
 template <class... KArgs, class... Args>
-bool launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, int smem, void* stream, Args... args) {
+bool launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, int smem, int cluster_y, void* stream,
+                const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // see grid_dependency_wait
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = cluster_y;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...) != cudaSuccess) {
+  cfg.numAttrs = cluster_y > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
     (void)cudaGetLastError();
     return false;
   }
@@ -890,21 +898,139 @@ static bool lora_plan_ok(const svdq_lora_plan* p) {
                                                                 p->groups).words);
 }
 
+// The workspace: kernel 13's U, then kernel 11's parts.
+struct LoraWorkspace {
+  size_t part, total;
+};
+static LoraWorkspace lora_workspace(const svdq_lora_plan* p, int K, int jr, int dev) {
+  LoraWorkspace w;
+  w.part = static_cast<size_t>(p->tiles) * svdq::kLoraTileRows * 2 * jr * sizeof(uint16_t);
+  w.total = w.part;
+  if (p->groups > 0)
+    w.total += static_cast<size_t>(p->groups) * lora_short_splits(p->groups, K, jr, dev) * svdq::kLoraGroupRows * jr *
+               sizeof(float);
+  w.total = std::max<size_t>(w.total, 16);
+  return w;
+}
+
 size_t svdq_lora_workspace_bytes(const svdq_lora_plan* plan, int K, int rank) {
   if (!lora_plan_ok(plan) || K <= 0 || K % 64 != 0 || rank <= 0 || rank % 16 != 0 ||
-      plan->slots * rank > svdq::kLoraMaxRank)
+      plan->slots * static_cast<int64_t>(rank) > svdq::kLoraMaxRank)
     return 0;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
     (void)cudaGetLastError();
     return 0;
   }
-  const int jr = plan->slots * rank;
-  size_t bytes = 16;
-  if (plan->groups > 0)
-    bytes += static_cast<size_t>(plan->groups) * lora_short_splits(plan->groups, K, jr, dev) * svdq::kLoraGroupRows *
-             jr * sizeof(float);
-  return bytes;
+  return lora_workspace(plan, K, plan->slots * rank, dev).total;
+}
+
+// One call's arguments, checked.
+struct LoraCall {
+  const void *X, *Yin, *A, *B;
+  void *Y, *ws, *stream;
+  int64_t ldx, ldyin, ldy;
+  const svdq_lora_plan* plan;
+  const int32_t *requests, *tiles, *groups;         // the plan's sections on the device
+  int M, N, K, rank, jr, dev;
+};
+
+// Kernels 13 and 14: the tiles of long requests, and (copy) of the rows to copy.
+static int lora_tiles_launch(const LoraCall& c, bool copy) {
+  namespace k13 = svdq::k13;
+  namespace k14 = svdq::k14;
+  const int tiles = c.plan->tiles, all = tiles + (copy ? c.plan->copy_tiles : 0);
+  const int jr = c.jr;
+  const int sms = sm_count(c.dev);
+  const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if (tiles > 0) {
+    k13::Params p;
+    p.tiles = c.tiles;
+    p.requests = c.requests;
+    p.U = static_cast<__nv_bfloat16*>(c.ws);
+    p.K = c.K;
+    p.rank = c.rank;
+    p.slots = c.plan->slots;
+    p.adapters = c.plan->adapters;
+    p.stages = std::min(k13::kMaxStages, (k13::kSmemMax - 2048) / k13::stage_bytes(jr));
+    // CTAs that share a tile's K: as many (1, 2, 4, 8) as keep the grid within one wave at two CTAs per SM
+    p.ks = 1;
+    while (p.ks < 8 && 2 * p.ks <= c.K / 64 && static_cast<int64_t>(tiles) * 2 * p.ks <= 2 * sms) p.ks *= 2;
+    const int smem = k13::smem_bytes(jr, p.stages);
+    CUtensorMap tX, tA;
+    if (!make_tmap(&tX, c.X, bf, 2, c.M, c.K, k13::kChunk, 32, CU_TENSOR_MAP_SWIZZLE_128B, c.ldx) ||
+        !make_tmap(&tA, c.A, bf, 2, static_cast<uint64_t>(p.adapters) * c.rank, c.K, k13::kChunk, c.rank,
+                   CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !set_smem_once<k13::lora_tile_down_kernel>(k13::kSmemMax, c.dev))
+      return SVDQ_ERR_CUDA;
+    if (!launch_pdl(k13::lora_tile_down_kernel, dim3(tiles, p.ks), k13::kThreads, smem, p.ks, c.stream, tX, tA, p))
+      return SVDQ_ERR_CUDA;
+  }
+  k14::Params p;
+  p.tiles = c.tiles;
+  p.requests = c.requests;
+  p.Yin = static_cast<const __nv_bfloat16*>(c.Yin);
+  p.Y = static_cast<__nv_bfloat16*>(c.Y);
+  p.ldy = c.ldy;
+  p.ntiles = tiles;
+  p.N = c.N;
+  p.BN = jr >= 64 ? 64 : 128;
+  p.chunks = (c.N + p.BN - 1) / p.BN;
+  p.items = all * p.chunks;
+  p.rank = c.rank;
+  p.slots = c.plan->slots;
+  p.adapters = c.plan->adapters;
+  p.wu = 2 * jr % 64 == 0 ? 64 : 32;
+  p.wb = c.rank % 64 == 0 ? 64 : c.rank % 32 == 0 ? 32 : 16;
+  p.early = tiles > 0;
+  const k14::Smem one = k14::smem_of(jr, p.BN, 1);
+  p.stages = std::min(k14::kMaxStages, (227 * 1024 - k14::smem_extra() - one.u) / one.stage);
+  const int smem = k14::smem_of(jr, p.BN, p.stages).bar + k14::smem_extra();
+  auto swizzle = [](int w) {
+    return w == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : w == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
+  };
+  CUtensorMap tU, tB, tYin, tY;
+  if (!make_tmap(&tYin, c.Yin, bf, 2, c.M, c.N, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B, c.ldyin) ||
+      !make_tmap(&tY, c.Y, bf, 2, c.M, c.N, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B, c.ldy))
+    return SVDQ_ERR_CUDA;
+  tU = tB = tY;                                     // not read when every tile is a copy
+  if (tiles > 0 &&
+      (!make_tmap(&tU, c.ws, bf, 2, static_cast<uint64_t>(tiles) * k14::kRows, 2 * jr, p.wu, k14::kRows, swizzle(p.wu)) ||
+       !make_tmap(&tB, c.B, bf, 2, static_cast<uint64_t>(p.adapters) * c.N, c.rank, p.wb, p.BN, swizzle(p.wb))))
+    return SVDQ_ERR_CUDA;
+  if (!set_smem_once<k14::lora_tile_up_kernel>(227 * 1024, c.dev)) return SVDQ_ERR_CUDA;
+  if (!launch_pdl(k14::lora_tile_up_kernel, dim3(std::min(p.items, sms)), k14::kThreads, smem, 1, c.stream, tU, tB,
+                  tYin, tY, p))
+    return SVDQ_ERR_CUDA;
+  return SVDQ_OK;
+}
+
+// Kernels 11 and 12: the groups of short requests.
+static int lora_groups_launch(const LoraCall& c, float* part) {
+  namespace k11 = svdq::k11;
+  k11::Params p;
+  p.X = static_cast<const __nv_bfloat16*>(c.X);
+  p.A = static_cast<const __nv_bfloat16*>(c.A);
+  p.B = static_cast<const __nv_bfloat16*>(c.B);
+  p.Yin = static_cast<const __nv_bfloat16*>(c.Yin);
+  p.Y = static_cast<__nv_bfloat16*>(c.Y);
+  p.ldx = c.ldx;
+  p.ldyin = c.ldyin;
+  p.ldy = c.ldy;
+  p.groups = c.groups;
+  p.part = part;
+  p.N = c.N;
+  p.K = c.K;
+  p.rank = c.rank;
+  p.slots = c.plan->slots;
+  p.ks = lora_short_splits(c.plan->groups, c.K, c.jr, c.dev);
+  if (!launch_pdl(k11::lora_short_down_kernel, dim3(c.plan->groups, c.jr / 16, p.ks), k11::kThreads, 0, 1, c.stream, p))
+    return SVDQ_ERR_CUDA;
+  const int strips = (c.N / 16 + k11::kWarps - 1) / k11::kWarps;
+  const int ny = std::max(1, std::min(strips, 8 * sm_count(c.dev) / c.plan->groups));
+  if (!launch_pdl(k11::lora_short_up_kernel, dim3(c.plan->groups, ny), k11::kThreads, 0, 1, c.stream, p))
+    return SVDQ_ERR_CUDA;
+  return SVDQ_OK;
 }
 
 int svdq_lora_add(const void* X, int64_t ldx, const void* Yin, int64_t ldyin, const void* A, const void* B,
@@ -912,6 +1038,11 @@ int svdq_lora_add(const void* X, int64_t ldx, const void* Yin, int64_t ldyin, co
                   void* workspace, size_t workspace_bytes, void* Y, int64_t ldy, void* stream) {
   if (M < 0 || N <= 0 || K <= 0 || rank <= 0 || !lora_plan_ok(plan) || plan->M != M) return SVDQ_ERR_INVALID_ARG;
   if (rank % 16 != 0 || plan->slots * static_cast<int64_t>(rank) > svdq::kLoraMaxRank || K % 64 != 0 || N % 64 != 0)
+    return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  // tile coordinates and piece counts are 32-bit
+  const int64_t all_tiles = static_cast<int64_t>(plan->tiles) + plan->copy_tiles;
+  if (static_cast<int64_t>(plan->adapters) * N > INT32_MAX - N || all_tiles * (N / 64) > INT32_MAX ||
+      all_tiles * svdq::kLoraTileRows > INT32_MAX)
     return SVDQ_ERR_UNSUPPORTED_SHAPE;
   if (M == 0) return SVDQ_OK;
   if (!Yin || !Y || !aligned16(Yin) || !aligned16(Y) || ldyin < N || ldy < N || ldyin % 8 != 0 || ldy % 8 != 0)
@@ -928,45 +1059,17 @@ int svdq_lora_add(const void* X, int64_t ldx, const void* Yin, int64_t ldyin, co
   }
   int dev;
   if (int st = current_device_ok(&dev)) return st;
-  if (work && workspace_bytes < svdq_lora_workspace_bytes(plan, K, rank)) return SVDQ_ERR_INVALID_ARG;
+  const LoraWorkspace ws = lora_workspace(plan, K, plan->slots * rank, dev);
+  if (work && workspace_bytes < ws.total) return SVDQ_ERR_INVALID_ARG;
 
-  const svdq::LoraLayout L =
-      svdq::lora_layout(plan->requests, plan->slots, static_cast<size_t>(plan->tiles) + plan->copy_tiles, plan->groups);
+  const svdq::LoraLayout L = svdq::lora_layout(plan->requests, plan->slots, all_tiles, plan->groups);
   const int32_t* words = static_cast<const int32_t*>(plan_dev);
-  const int jr = plan->slots * rank;
-  namespace k11 = svdq::k11;
-  if (plan->copy_tiles > 0 && !in_place) {
-    const int tiles_n = std::max(1, std::min(16, 4 * sm_count(dev) / plan->copy_tiles));
-    if (!launch_pdl(k11::lora_copy_kernel, dim3(plan->copy_tiles, tiles_n), k11::kThreads, 0, stream,
-                    static_cast<const __nv_bfloat16*>(Yin), static_cast<long long>(ldyin),
-                    static_cast<__nv_bfloat16*>(Y), static_cast<long long>(ldy), N,
-                    words + L.tiles + 4 * static_cast<size_t>(plan->tiles)))
-      return SVDQ_ERR_CUDA;
-  }
-  if (plan->groups > 0) {
-    k11::Params p;
-    p.X = static_cast<const __nv_bfloat16*>(X);
-    p.A = static_cast<const __nv_bfloat16*>(A);
-    p.B = static_cast<const __nv_bfloat16*>(B);
-    p.Yin = static_cast<const __nv_bfloat16*>(Yin);
-    p.Y = static_cast<__nv_bfloat16*>(Y);
-    p.ldx = ldx;
-    p.ldyin = ldyin;
-    p.ldy = ldy;
-    p.groups = words + L.groups;
-    p.part = static_cast<float*>(workspace);
-    p.N = N;
-    p.K = K;
-    p.rank = rank;
-    p.slots = plan->slots;
-    p.ks = lora_short_splits(plan->groups, K, jr, dev);
-    if (!launch_pdl(k11::lora_short_down_kernel, dim3(plan->groups, jr / 16, p.ks), k11::kThreads, 0, stream, p))
-      return SVDQ_ERR_CUDA;
-    const int strips = (N / 16 + k11::kWarps - 1) / k11::kWarps;
-    const int ny = std::max(1, std::min(strips, 8 * sm_count(dev) / plan->groups));
-    if (!launch_pdl(k11::lora_short_up_kernel, dim3(plan->groups, ny), k11::kThreads, 0, stream, p))
-      return SVDQ_ERR_CUDA;
-  }
+  const LoraCall c{X,   Yin, A,     B,    Y, workspace, stream, ldx,  ldyin,
+                   ldy, plan, words + L.requests, words + L.tiles, words + L.groups, M, N, K, rank, plan->slots * rank, dev};
+  if (plan->tiles > 0 || (plan->copy_tiles > 0 && !in_place))
+    if (int st = lora_tiles_launch(c, !in_place)) return st;
+  if (plan->groups > 0)
+    if (int st = lora_groups_launch(c, reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ws.part))) return st;
   return launch_status();
 }
 
@@ -1101,7 +1204,7 @@ int svdq_qk_norm_rope(const void* Q, int64_t q_row_stride, int64_t q_head_stride
 #define SVDQ_ROPE_CASE(V_, L_)                                                                                  \
   if (V == V_ && lpr == L_)                                                                                     \
     return launch_pdl(pairing ? k9::qk_norm_rope_kernel<V_, L_, true> : k9::qk_norm_rope_kernel<V_, L_, false>, \
-                      grid, k9::kThreads, 0, stream, p, fr)                                                     \
+                      grid, k9::kThreads, 0, 1, stream, p, fr)                                                     \
                ? launch_status()                                                                                \
                : SVDQ_ERR_CUDA
   SVDQ_ROPE_CASE(8, 1);
@@ -1146,7 +1249,7 @@ int svdq_rope_axes_tables(const void* positions, int positions_float, int P, int
   // pairs per thread: the fewest that keep the grid within eight blocks per SM
   const int by = std::max(1, std::min(p.pairs, 8 * sm_count(dev) / bx));
   p.per = (p.pairs + by - 1) / by;
-  if (!launch_pdl(k9::rope_tables_kernel, dim3(bx, (p.pairs + p.per - 1) / p.per), k9::kThreads, 0, stream, p, fr))
+  if (!launch_pdl(k9::rope_tables_kernel, dim3(bx, (p.pairs + p.per - 1) / p.per), k9::kThreads, 0, 1, stream, p, fr))
     return SVDQ_ERR_CUDA;
   return launch_status();
 }

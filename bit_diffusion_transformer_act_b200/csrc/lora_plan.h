@@ -24,7 +24,7 @@ constexpr int kLoraMaxSlots = 8;
 constexpr int kLoraMaxRank = 128;          // slots x rank
 constexpr int kLoraGroupRows = 16;
 constexpr int kLoraTileRows = 128;
-constexpr int kLoraShortRows = 1 << 30;     // requests of at most this many rows are gathered into groups
+constexpr int kLoraShortRows = 16;          // requests of at most this many rows are gathered into groups
 
 struct LoraLayout {
   size_t requests, tiles, groups, words;   // word offsets; words in all

@@ -178,20 +178,5 @@ lora_short_up_kernel(const Params p) {
   }
 }
 
-// Rows that no adapter touches, when the output is not y itself.
-__global__ void __launch_bounds__(kThreads)
-lora_copy_kernel(const __nv_bfloat16* yin, long long ldyin, __nv_bfloat16* y, long long ldy, int N,
-                 const int32_t* tiles) {
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const int row0 = tiles[blockIdx.x * 4], nrows = tiles[blockIdx.x * 4 + 1];
-  const int per_row = N / 8;
-  for (long long i = threadIdx.x + static_cast<long long>(blockIdx.y) * kThreads;
-       i < static_cast<long long>(nrows) * per_row; i += static_cast<long long>(gridDim.y) * kThreads) {
-    const long long row = row0 + i / per_row, c = i % per_row * 8;
-    *reinterpret_cast<uint4*>(y + row * ldy + c) = *reinterpret_cast<const uint4*>(yin + row * ldyin + c);
-  }
-}
-
 }  // namespace k11
 }  // namespace svdq

@@ -1,0 +1,504 @@
+// Kernels 13 and 14: the adapters of long requests, in tiles of up to 128 rows of one request.
+//
+// Mathematics.  out[m] = y[m] + sum_j B_j (w_j A_j x[m]).  Kernel 13 forms the tile's U = X [A_0; A_1; ...]^T
+// (128 x slots rank, fp32), scales column block j by the request's w_j and stores it as a high and a
+// low bf16 part side by side (U = hi + lo to 2^-16 relative).  Kernel 14 forms [hi | lo] [B_0 B_1 ... | B_0
+// B_1 ...]^T for a 128 x BN piece of the output, adds y and rounds once.
+//
+// What bounds them: memory.  With slots rank = 64 a row of X costs 2 K bytes and 2 K 64 flops, 64 flops per
+// byte, and a value of Y 4 bytes and 256 flops -- against 265 flops per byte of the card.  So the MMAs only
+// have to stay out of the way, and both kernels are streams: X through kernel 13, Y through kernel 14, each
+// once; A, B and U come from L2.
+//
+// Kernel 13: the CTAs of a cluster share a tile's K and sum their U over distributed shared memory in
+// slice order (no atomics, no scratch).  Kernel 14 is persistent: a CTA owns a run of (tile, BN columns)
+// pieces with the columns running first, so U is loaded once per tile; y and B arrive by TMA in a ring of
+// stages, the sum overwrites y in its stage, and the stage is stored from there.  32-row slabs that the
+// tile fills go out by TMA, a last partial slab row by row.  Rows of other requests in a partial tile are never
+// stored; each row of an MMA's result depends on its own row of the left operand only.
+//
+// Every mbarrier wait is bounded (see ptx.cuh).
+#pragma once
+
+#include "lora_plan.h"
+#include "lora_short.cuh"
+#include "ptx.cuh"
+
+namespace svdq {
+namespace k13 {
+
+constexpr int kRows = kLoraTileRows;
+constexpr int kChunk = 64;
+constexpr int kThreads = 128;
+constexpr int kMaxStages = 6;
+constexpr int kXBytes = kRows * kChunk * 2;
+constexpr int kTmemCols = 128;
+constexpr int kSmemMax = 112 * 1024;                // two CTAs per SM
+
+struct Params {
+  const int32_t* tiles;                             // {first row, rows, request, 0}
+  const int32_t* requests;                          // [requests][2 slots]: ids, weights
+  __nv_bfloat16* U;                                 // [tiles][128][2 slots rank]
+  int K, rank, slots, adapters, ks, stages;
+};
+
+// kind::f16 instruction descriptor: D f32, A and B bf16, K-major, M = 128.
+__device__ __forceinline__ uint32_t idesc_bf16(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+__host__ __device__ constexpr int stage_bytes(int jr) { return kXBytes + jr * kChunk * 2; }
+__host__ __device__ constexpr int body_bytes(int jr, int stages) {      // the ring, later the partial U
+  const int ring = stages * stage_bytes(jr), part = kRows * (jr + 4) * 4;
+  return ring > part ? ring : part;
+}
+constexpr int smem_bytes(int jr, int stages) { return 1024 + (body_bytes(jr, stages) + 15) / 16 * 16 + 8 * (2 * kMaxStages + 2) + 16; }
+
+__global__ void __launch_bounds__(kThreads)
+lora_tile_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
+                      const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const int jr = p.slots * p.rank;
+  const int S = p.stages;
+  const uint32_t off_bar = static_cast<uint32_t>((body_bytes(jr, S) + 15) / 16 * 16);
+  const uint32_t bars = base + off_bar;
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (kMaxStages + s); };
+  const uint32_t acc_full = bars + 8u * (2 * kMaxStages);
+  const uint32_t drain = acc_full + 8u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + off_bar + 8 * (2 * kMaxStages + 2));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int nck_all = p.K / kChunk;
+  const int c0 = static_cast<int>(static_cast<long long>(nck_all) * blockIdx.y / p.ks);
+  const int nck = static_cast<int>(static_cast<long long>(nck_all) * (blockIdx.y + 1) / p.ks) - c0;   // >= 1: ks <= K / 64
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < S; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
+    mbar_init(acc_full, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmX);
+    prefetch_tmap(&tmA);
+  }
+  if (warp == 1) tmem_alloc<kTmemCols>(smem_addr(tmem_slot));
+  grid_dependency_wait();                           // X (or the plan, or an adapter) may come from the previous kernel
+  grid_launch_dependents();                         // kernel 14 counts on this coming after the wait
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int4 tile = *reinterpret_cast<const int4*>(p.tiles + static_cast<size_t>(blockIdx.x) * 4);
+  const int32_t* req = p.requests + static_cast<size_t>(tile.z) * 2 * p.slots;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer
+    const int slabs = (tile.y + 31) / 32;
+    for (int c = 0; c < nck; ++c) {
+      const int s = c % S;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty(s), ((c / S) & 1u) ^ 1u, abort_flag, 71))) break;
+      if (elect_one()) {
+        const uint32_t sb = base + s * stage_bytes(jr);
+        mbar_arrive_expect_tx(full(s), slabs * 4096 + jr * kChunk * 2);
+        for (int i = 0; i < slabs; ++i) tma_load_2d(sb + i * 4096, &tmX, (c0 + c) * kChunk, tile.x + 32 * i, full(s));
+        for (int j = 0; j < p.slots; ++j) {
+          const int id = req[j];                    // an empty slot's rows lie past the pool: read as zeros
+          tma_load_2d(sb + kXBytes + j * p.rank * kChunk * 2, &tmA, (c0 + c) * kChunk,
+                      (id < 0 ? p.adapters : id) * p.rank, full(s));
+        }
+      }
+      __syncwarp();
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issue (one elected lane)
+    constexpr uint32_t kHiSw128 = smem_desc_hi(1024, 2);
+    constexpr uint32_t kLbo = 1u << 16;
+    const uint32_t idesc = idesc_bf16(jr);
+    for (int c = 0; c < nck; ++c) {
+      const int s = c % S;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(full(s), (c / S) & 1u, abort_flag, 72))) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t sb = base + s * stage_bytes(jr);
+        const uint32_t a_lo = (sb >> 4) | kLbo, b_lo = ((sb + kXBytes) >> 4) | kLbo;
+#pragma unroll
+        for (int kk = 0; kk < kChunk / 16; ++kk)
+          umma_bf16(tmem, make_desc(a_lo + kk * 2, kHiSw128), make_desc(b_lo + kk * 2, kHiSw128), idesc,
+                    (c | kk) != 0 ? 1u : 0u);
+        tc_commit(empty(s));
+        if (c == nck - 1) tc_commit(acc_full);
+      }
+      __syncwarp();
+    }
+  }
+
+  // ---------------------------------------------------------------- U, summed over the cluster
+  // The last commit covers every MMA, and with them every copy into the ring: its space is free.
+  const int stride = jr + 4;                        // floats per row: 16-byte stores of 8 rows fall on all banks
+  float* part = reinterpret_cast<float*>(gbase);
+  {
+    const int row = warp * 32 + lane;
+    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(acc_full, 0, abort_flag, 73));
+    tc_fence_after();
+    for (int c = 0; ok && c < jr; c += 32) {
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+      tmem_wait_ld_regs(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + 4 * j < jr)
+          *reinterpret_cast<float4*>(part + row * stride + c + 4 * j) =
+              make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]), __uint_as_float(v[4 * j + 2]),
+                          __uint_as_float(v[4 * j + 3]));
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  cluster_sync_all();                               // every slice's partial is in its CTA's shared memory
+  const int rpc = kRows / p.ks;
+  const int pieces = jr / 4;
+  for (int i = threadIdx.x; i < rpc * pieces; i += kThreads) {
+    const int r = static_cast<int>(cluster_ctarank()) * rpc + i / pieces, c = i % pieces * 4;
+    if (r >= tile.y) continue;
+    float4 v[8];
+#pragma unroll
+    for (int z = 0; z < 8; ++z)
+      if (z < p.ks) v[z] = ld_dsmem_f32x4(part + r * stride + c, static_cast<uint32_t>(z));
+    float4 u = v[0];
+#pragma unroll
+    for (int z = 1; z < 8; ++z)                     // in slice order
+      if (z < p.ks) { u.x += v[z].x; u.y += v[z].y; u.z += v[z].z; u.w += v[z].w; }
+    const int slot = c / p.rank;
+    const bool has = req[slot] >= 0;                // an empty slot adds nothing, whatever is in X
+    const float w = __int_as_float(req[p.slots + slot]);
+    const float uu[4] = {has ? u.x * w : 0.f, has ? u.y * w : 0.f, has ? u.z * w : 0.f, has ? u.w * w : 0.f};
+    uint32_t h[4];
+    float lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = k11::split_hi_lo(uu[j], lo[j]);
+    __nv_bfloat16* dst = p.U + (static_cast<size_t>(blockIdx.x) * kRows + r) * (2 * jr) + c;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+    *reinterpret_cast<uint2*>(dst + jr) = make_uint2(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]));
+  }
+  if (*abort_flag) {
+    // a wait ran out: let the MMAs and copies already issued finish before the memory goes away
+    if (warp == 1) {
+      if (elect_one()) tc_commit(drain);
+      __syncwarp();
+      mbar_wait_bounded(drain, 0, nullptr, 74);
+    }
+    if (warp == 0 && lane == 0) {
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 2000000ull) { }
+    }
+  }
+  __syncwarp();
+  cluster_sync_all();                               // the peers have read this CTA's partial
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<kTmemCols>(tmem);
+  }
+}
+
+}  // namespace k13
+
+namespace k14 {
+
+constexpr int kRows = kLoraTileRows;
+constexpr int kThreads = 192;                       // producer, MMA, four epilogue warps
+constexpr int kMaxStages = 6;
+constexpr int kTmemCols = 256;                      // two accumulators of up to 128 columns
+
+struct Params {
+  const int32_t* tiles;
+  const int32_t* requests;
+  const __nv_bfloat16* Yin;
+  __nv_bfloat16* Y;
+  long long ldy;
+  int ntiles;                                       // tiles with adapters; tiles after them are copied
+  int items, chunks;                                // (tile, BN columns) pieces; pieces per tile
+  int N, BN, rank, slots, adapters, stages;
+  int wu, wb;                                       // columns per box of U and of B: 64, 32 or 16
+  int early;                                        // y, B and the plan are complete before this grid's dependency
+};
+
+// Shared memory (1024-byte aligned): U | stages of (B, y) | barriers.
+struct Smem {
+  int u, b, y, stage, bar;
+};
+__host__ __device__ inline Smem smem_of(int jr, int BN, int stages) {
+  Smem m;
+  m.u = kRows * 2 * jr * 2;
+  m.b = BN * jr * 2;
+  m.y = kRows * BN * 2;
+  m.stage = m.b + m.y;
+  m.bar = m.u + stages * m.stage;
+  return m;
+}
+constexpr int kNumBars = 2 * kMaxStages + 7;        // full, empty, u_full, u_empty, acc_full[2], acc_empty[2], drain
+constexpr int smem_extra() { return 1024 + 8 * kNumBars + 16; }
+
+// Descriptor words of a K-major tile stored as boxes of w columns (128-, 64- or 32-byte swizzle).
+struct Boxes {
+  uint32_t hi, box_bytes;
+  int w;
+};
+__device__ __forceinline__ Boxes boxes(int w, int rows) {
+  Boxes b;
+  b.w = w;
+  b.box_bytes = static_cast<uint32_t>(rows * w * 2);
+  b.hi = w == 64 ? smem_desc_hi(1024, 2) : w == 32 ? smem_desc_hi(512, 4) : smem_desc_hi(256, 6);
+  return b;
+}
+__device__ __forceinline__ uint64_t box_desc(const Boxes& b, uint32_t at, int col) {
+  return make_desc(((at + col / b.w * b.box_bytes + col % b.w * 2) >> 4) | (1u << 16), b.hi);
+}
+
+__global__ void __launch_bounds__(kThreads)
+lora_tile_up_kernel(const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmYin, const __grid_constant__ CUtensorMap tmY,
+                    const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const int jr = p.slots * p.rank;
+  const int S = p.stages;
+  const Smem sm = smem_of(jr, p.BN, S);
+  const uint32_t bars = base + sm.bar;
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (kMaxStages + s); };
+  const uint32_t u_full = bars + 8u * (2 * kMaxStages), u_empty = u_full + 8u;
+  auto acc_full = [&](int b) { return u_full + 16u + 8u * b; };
+  auto acc_empty = [&](int b) { return u_full + 32u + 8u * b; };
+  const uint32_t drain = u_full + 48u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + sm.bar + 8 * kNumBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int i0 = static_cast<int>(static_cast<long long>(p.items) * blockIdx.x / gridDim.x);
+  const int i1 = static_cast<int>(static_cast<long long>(p.items) * (blockIdx.x + 1) / gridDim.x);
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < S; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 5); }   // four epilogue warps, the MMAs
+    mbar_init(u_full, 1);
+    mbar_init(u_empty, 1);
+    for (int b = 0; b < 2; ++b) { mbar_init(acc_full(b), 1); mbar_init(acc_empty(b), 4); }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmU);
+    prefetch_tmap(&tmB);
+    prefetch_tmap(&tmYin);
+    prefetch_tmap(&tmY);
+  }
+  if (warp == 1) tmem_alloc<kTmemCols>(smem_addr(tmem_slot));
+  if (!p.early) grid_dependency_wait();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto tile_of = [&](int t) { return __ldcg(reinterpret_cast<const int4*>(p.tiles) + t); };
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer
+    // With early, y, B and the plan are older than kernel 13 (which let this grid start after its own
+    // dependency wait): their loads go out at once, and only U waits for kernel 13.
+    bool waited = !p.early;
+    int last = -1, it = 0, nu = 0;
+    for (int i = i0; i < i1; ++i, ++it) {
+      const int t = i / p.chunks, n0 = i % p.chunks * p.BN;
+      const int s = it % S;
+      const int4 tile = tile_of(t);
+      const bool busy = t < p.ntiles;
+      const bool new_u = busy && t != last;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty(s), ((it / S) & 1u) ^ 1u, abort_flag, 81))) break;
+      if (elect_one()) {
+        const int slabs = (tile.y + 31) / 32, halves = min(p.BN, p.N - n0) / 64;
+        const uint32_t sb = base + sm.u + s * sm.stage;
+        mbar_arrive_expect_tx(full(s), slabs * halves * 4096 + (busy ? sm.b : 0));
+        for (int h = 0; h < halves; ++h)
+          for (int q = 0; q < slabs; ++q)
+            tma_load_2d(sb + sm.b + (h * 4 + q) * 4096, &tmYin, n0 + 64 * h, tile.x + 32 * q, full(s));
+        if (busy) {
+          const int32_t* req = p.requests + static_cast<size_t>(tile.z) * 2 * p.slots;
+          uint32_t at = sb;
+          for (int j = 0; j < p.slots; ++j) {
+            const int id = __ldcg(req + j);         // an empty slot's rows lie past the pool: read as zeros
+            for (int c = 0; c < p.rank; c += p.wb, at += p.BN * p.wb * 2)
+              tma_load_2d(at, &tmB, c, id < 0 ? p.adapters * p.N : id * p.N + n0, full(s));
+          }
+        }
+      }
+      __syncwarp();
+      if (new_u) {
+        if (!waited) {
+          grid_dependency_wait();
+          waited = true;
+        }
+        // the previous tile's MMAs have read U
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(u_empty, (nu & 1u) ^ 1u, abort_flag, 82))) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(u_full, sm.u);
+          for (int c = 0; c < 2 * jr; c += p.wu)
+            tma_load_2d(base + c * kRows * 2, &tmU, c, t * kRows, u_full);
+        }
+        __syncwarp();
+        last = t;
+        ++nu;
+      }
+    }
+    if (!waited) grid_dependency_wait();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issue (one elected lane)
+    const uint32_t idesc = k13::idesc_bf16(p.BN);
+    const Boxes bu = boxes(p.wu, kRows), bb = boxes(p.wb, p.BN);
+    int last = -1, it = 0, nu = 0, na = 0;
+    for (int i = i0; i < i1; ++i, ++it) {
+      const int t = i / p.chunks;
+      const int s = it % S;
+      if (t >= p.ntiles) {                          // a copied piece: no MMA reads this stage
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(full(s), (it / S) & 1u, abort_flag, 83))) break;
+        if (lane == 0) mbar_arrive(empty(s));
+        continue;
+      }
+      const int b = na & 1;
+      bool ok = true;
+      if (t != last) {
+        ok = mbar_wait_bounded(u_full, nu & 1u, abort_flag, 84);
+        last = t;
+        ++nu;
+      }
+      ok = ok && mbar_wait_bounded(full(s), (it / S) & 1u, abort_flag, 85);
+      ok = ok && mbar_wait_bounded(acc_empty(b), ((na >> 1) & 1u) ^ 1u, abort_flag, 86);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t sb = base + sm.u + s * sm.stage;
+        for (int c = 0; c < 2 * jr; c += 16)
+          umma_bf16(tmem + static_cast<uint32_t>(b * 128), box_desc(bu, base, c), box_desc(bb, sb, c < jr ? c : c - jr),
+                    idesc, c != 0 ? 1u : 0u);
+        tc_commit(acc_full(b));
+        tc_commit(empty(s));
+        if (i + 1 == i1 || (i + 1) / p.chunks != t) tc_commit(u_empty);
+      }
+      __syncwarp();
+      ++na;
+    }
+  } else {
+    // ---------------------------------------------------------------- epilogue
+    const int q = warp & 3;                         // tensor-memory lane quarter = 32-row slab of the tile
+    const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const uint32_t sw = static_cast<uint32_t>(lane & 7);
+    int it = 0, na = 0, held = -1;                  // held: the stage whose store is still being read out
+    for (int i = i0; i < i1; ++i, ++it) {
+      const int t = i / p.chunks, n0 = i % p.chunks * p.BN;
+      const int s = it % S;
+      const int4 tile = tile_of(t);
+      const bool busy = t < p.ntiles;
+      const int b = na & 1;
+      bool ok = mbar_wait_bounded(full(s), (it / S) & 1u, abort_flag, 87);
+      if (busy) {
+        ok = ok && mbar_wait_bounded(acc_full(b), (na >> 1) & 1u, abort_flag, 88);
+        ++na;
+      }
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      tc_fence_after();
+      const int rows = min(32, tile.y - 32 * q);    // of this slab; none or fewer where the tile ends
+      const int halves = min(p.BN, p.N - n0) / 64;
+      const uint32_t yq = base + sm.u + s * sm.stage + sm.b + q * 4096;
+      if (rows > 0 && busy) {
+        for (int h = 0; h < 2 * halves; ++h) {      // 32 columns at a time
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(trow + static_cast<uint32_t>(b * 128 + 32 * h), v);
+          const uint32_t yrow = yq + (h >> 1) * 16384 + lane * 128;
+          uint4 y[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(y[c].x), "=r"(y[c].y), "=r"(y[c].z), "=r"(y[c].w)
+                         : "r"(yrow + (((4u * (h & 1) + c) ^ sw) << 4)));
+          tmem_wait_ld_regs(v);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(&y[c]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              w[j] = pack_bf16x2(bf16lo_to_f32(w[j]) + __uint_as_float(v[8 * c + 2 * j]),
+                                 bf16hi_to_f32(w[j]) + __uint_as_float(v[8 * c + 2 * j + 1]));
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                         ::"r"(yrow + (((4u * (h & 1) + c) ^ sw) << 4)), "r"(y[c].x), "r"(y[c].y), "r"(y[c].z),
+                           "r"(y[c].w)
+                         : "memory");
+          }
+        }
+      }
+      if (busy) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty(b));   // the accumulator has been read
+      }
+      if (rows == 32) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+          for (int h = 0; h < halves; ++h) tma_store_2d(&tmY, yq + h * 16384, n0 + 64 * h, tile.x + 32 * q);
+      } else if (rows > 0) {
+        __syncwarp();
+        for (int h = 0; h < halves; ++h)
+          for (int r = lane / 8; r < rows; r += 4) {   // eight lanes write a row's 128 bytes
+            const uint32_t c = static_cast<uint32_t>(lane & 7);
+            uint4 v;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(yq + h * 16384 + r * 128 + ((c ^ (static_cast<uint32_t>(r) & 7u)) << 4)) : "memory");
+            *reinterpret_cast<uint4*>(p.Y + (tile.x + 32 * q + r) * p.ldy + n0 + 64 * h + 8 * c) = v;
+          }
+      }
+      // hand the previous piece's stage back once its store has read it
+      if (lane == 0) {
+        bulk_commit_group();
+        bulk_wait_group_read<1>();
+        if (held >= 0) mbar_arrive(empty(held));
+      }
+      held = s;
+      __syncwarp();
+    }
+    if (lane == 0) {
+      bulk_wait_group_read<0>();
+      if (held >= 0) mbar_arrive(empty(held));
+      bulk_wait_group<0>();
+    }
+    __syncwarp();
+  }
+  grid_launch_dependents();
+
+  __syncthreads();
+  if (*abort_flag) {
+    if (warp == 1) {
+      if (elect_one()) tc_commit(drain);
+      __syncwarp();
+      mbar_wait_bounded(drain, 0, nullptr, 89);
+    }
+    if (warp == 0 && lane == 0) {
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 2000000ull) { }
+    }
+    __syncthreads();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<kTmemCols>(tmem);
+  }
+}
+
+}  // namespace k14
+}  // namespace svdq
