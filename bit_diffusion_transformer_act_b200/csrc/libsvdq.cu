@@ -952,55 +952,53 @@ static int lora_tiles_launch(const LoraCall& c, bool copy) {
     p.rank = c.rank;
     p.slots = c.plan->slots;
     p.adapters = c.plan->adapters;
-    p.stages = std::min(k13::kMaxStages, (k13::kSmemMax - 2048) / k13::stage_bytes(jr));
-    // CTAs that share a tile's K: as many (1, 2, 4, 8) as keep the grid within one wave at two CTAs per SM
+    p.stages = std::min(k13::kMaxStages, std::max(2, (k13::kSmemMax - 2048) / k13::stage_bytes(jr)));
+    // CTAs that share a tile's K: the most (1, 2, 4, 8) that keep the grid within one wave at three CTAs per
+    // SM; a cluster's CTAs share a GPC, whose odd SMs leave room for fewer of the larger ones
     p.ks = 1;
-    while (p.ks < 8 && 2 * p.ks <= c.K / 64 && static_cast<int64_t>(tiles) * 2 * p.ks <= 2 * sms) p.ks *= 2;
+    while (p.ks < 8 && 2 * p.ks <= c.K / 64 && static_cast<int64_t>(tiles) * 2 * p.ks <= 3 * sms * 7 / 8) p.ks *= 2;
     const int smem = k13::smem_bytes(jr, p.stages);
-    CUtensorMap tX, tA;
+    CUtensorMap tX, tX128, tA;
     if (!make_tmap(&tX, c.X, bf, 2, c.M, c.K, k13::kChunk, 32, CU_TENSOR_MAP_SWIZZLE_128B, c.ldx) ||
+        !make_tmap(&tX128, c.X, bf, 2, c.M, c.K, k13::kChunk, 128, CU_TENSOR_MAP_SWIZZLE_128B, c.ldx) ||
         !make_tmap(&tA, c.A, bf, 2, static_cast<uint64_t>(p.adapters) * c.rank, c.K, k13::kChunk, c.rank,
                    CU_TENSOR_MAP_SWIZZLE_128B) ||
         !set_smem_once<k13::lora_tile_down_kernel>(k13::kSmemMax, c.dev))
       return SVDQ_ERR_CUDA;
-    if (!launch_pdl(k13::lora_tile_down_kernel, dim3(tiles, p.ks), k13::kThreads, smem, p.ks, c.stream, tX, tA, p))
+    if (!launch_pdl(k13::lora_tile_down_kernel, dim3(tiles, p.ks), k13::kThreads, smem, p.ks, c.stream, tX, tX128, tA, p))
       return SVDQ_ERR_CUDA;
   }
   k14::Params p;
   p.tiles = c.tiles;
   p.requests = c.requests;
-  p.Yin = static_cast<const __nv_bfloat16*>(c.Yin);
+  p.U = static_cast<const __nv_bfloat16*>(c.ws);
   p.Y = static_cast<__nv_bfloat16*>(c.Y);
   p.ldy = c.ldy;
   p.ntiles = tiles;
   p.N = c.N;
-  p.BN = jr >= 64 ? 64 : 128;
-  p.chunks = (c.N + p.BN - 1) / p.BN;
+  p.chunks = (c.N + k14::kBN - 1) / k14::kBN;
   p.items = all * p.chunks;
   p.rank = c.rank;
   p.slots = c.plan->slots;
   p.adapters = c.plan->adapters;
-  p.wu = 2 * jr % 64 == 0 ? 64 : 32;
   p.wb = c.rank % 64 == 0 ? 64 : c.rank % 32 == 0 ? 32 : 16;
   p.early = tiles > 0;
-  const k14::Smem one = k14::smem_of(jr, p.BN, 1);
-  p.stages = std::min(k14::kMaxStages, (227 * 1024 - k14::smem_extra() - one.u) / one.stage);
-  const int smem = k14::smem_of(jr, p.BN, p.stages).bar + k14::smem_extra();
+  p.stages = std::min(k14::kMaxStages, (227 * 1024 - k14::kSmemExtra) / k14::stage_bytes(jr));
+  const int smem = p.stages * k14::stage_bytes(jr) + k14::kSmemExtra;
   auto swizzle = [](int w) {
     return w == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : w == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
   };
-  CUtensorMap tU, tB, tYin, tY;
+  CUtensorMap tB, tYin, tYin128, tY;
   if (!make_tmap(&tYin, c.Yin, bf, 2, c.M, c.N, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B, c.ldyin) ||
+      !make_tmap(&tYin128, c.Yin, bf, 2, c.M, c.N, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, c.ldyin) ||
       !make_tmap(&tY, c.Y, bf, 2, c.M, c.N, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B, c.ldy))
     return SVDQ_ERR_CUDA;
-  tU = tB = tY;                                     // not read when every tile is a copy
-  if (tiles > 0 &&
-      (!make_tmap(&tU, c.ws, bf, 2, static_cast<uint64_t>(tiles) * k14::kRows, 2 * jr, p.wu, k14::kRows, swizzle(p.wu)) ||
-       !make_tmap(&tB, c.B, bf, 2, static_cast<uint64_t>(p.adapters) * c.N, c.rank, p.wb, p.BN, swizzle(p.wb))))
+  tB = tY;                                          // not read when every tile is a copy
+  if (tiles > 0 && !make_tmap(&tB, c.B, bf, 2, static_cast<uint64_t>(p.adapters) * c.N, c.rank, p.wb, k14::kBN, swizzle(p.wb)))
     return SVDQ_ERR_CUDA;
   if (!set_smem_once<k14::lora_tile_up_kernel>(227 * 1024, c.dev)) return SVDQ_ERR_CUDA;
-  if (!launch_pdl(k14::lora_tile_up_kernel, dim3(std::min(p.items, sms)), k14::kThreads, smem, 1, c.stream, tU, tB,
-                  tYin, tY, p))
+  if (!launch_pdl(k14::lora_tile_up_kernel, dim3(std::min(p.items, sms)), k14::kThreads, smem, 1, c.stream, tB, tYin,
+                  tYin128, tY, p))
     return SVDQ_ERR_CUDA;
   return SVDQ_OK;
 }

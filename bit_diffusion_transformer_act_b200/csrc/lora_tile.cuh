@@ -13,7 +13,8 @@
 // Kernel 13: the CTAs of a cluster share a tile's K and sum their U over distributed shared memory in
 // slice order (no atomics, no scratch).  Kernel 14 is persistent: a CTA owns a run of (tile, BN columns)
 // pieces with the columns running first, so U is loaded once per tile; y and B arrive by TMA in a ring of
-// stages, the sum overwrites y in its stage, and the stage is stored from there.  32-row slabs that the
+// stages, the sum overwrites y in its stage, and the stage is stored from there.  U is the left operand and
+// lives in tensor memory (two tiles of it), which leaves shared memory to the ring.  32-row slabs that the
 // tile fills go out by TMA, a last partial slab row by row.  Rows of other requests in a partial tile are never
 // stored; each row of an MMA's result depends on its own row of the left operand only.
 //
@@ -33,7 +34,7 @@ constexpr int kThreads = 128;
 constexpr int kMaxStages = 6;
 constexpr int kXBytes = kRows * kChunk * 2;
 constexpr int kTmemCols = 128;
-constexpr int kSmemMax = 112 * 1024;                // two CTAs per SM
+constexpr int kSmemMax = 74 * 1024;                 // three CTAs per SM
 
 struct Params {
   const int32_t* tiles;                             // {first row, rows, request, 0}
@@ -56,8 +57,8 @@ __host__ __device__ constexpr int body_bytes(int jr, int stages) {      // the r
 constexpr int smem_bytes(int jr, int stages) { return 1024 + (body_bytes(jr, stages) + 15) / 16 * 16 + 8 * (2 * kMaxStages + 2) + 16; }
 
 __global__ void __launch_bounds__(kThreads)
-lora_tile_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
-                      const Params p) {
+lora_tile_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmX128,
+                      const __grid_constant__ CUtensorMap tmA, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -85,6 +86,7 @@ lora_tile_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_cons
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tmX);
+    prefetch_tmap(&tmX128);
     prefetch_tmap(&tmA);
   }
   if (warp == 1) tmem_alloc<kTmemCols>(smem_addr(tmem_slot));
@@ -100,20 +102,27 @@ lora_tile_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_cons
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
     const int slabs = (tile.y + 31) / 32;
+    int a_row = 0;                                  // lane j: first row of slot j's adapter in A; an empty slot's
+    if (lane < p.slots) {                           // rows lie past the pool and are read as zeros
+      const int id = req[lane];
+      a_row = (id < 0 ? p.adapters : id) * p.rank;
+    }
     for (int c = 0; c < nck; ++c) {
       const int s = c % S;
+      const uint32_t sb = base + s * stage_bytes(jr);
       if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty(s), ((c / S) & 1u) ^ 1u, abort_flag, 71))) break;
       if (elect_one()) {
-        const uint32_t sb = base + s * stage_bytes(jr);
         mbar_arrive_expect_tx(full(s), slabs * 4096 + jr * kChunk * 2);
-        for (int i = 0; i < slabs; ++i) tma_load_2d(sb + i * 4096, &tmX, (c0 + c) * kChunk, tile.x + 32 * i, full(s));
-        for (int j = 0; j < p.slots; ++j) {
-          const int id = req[j];                    // an empty slot's rows lie past the pool: read as zeros
-          tma_load_2d(sb + kXBytes + j * p.rank * kChunk * 2, &tmA, (c0 + c) * kChunk,
-                      (id < 0 ? p.adapters : id) * p.rank, full(s));
-        }
+        if (slabs == 4) tma_load_2d(sb, &tmX128, (c0 + c) * kChunk, tile.x, full(s));
+        else
+          for (int i = 0; i < slabs; ++i) tma_load_2d(sb + i * 4096, &tmX, (c0 + c) * kChunk, tile.x + 32 * i, full(s));
       }
       __syncwarp();
+      for (int j = 0; j < p.slots; ++j) {
+        const int row = __shfl_sync(0xFFFFFFFFu, a_row, j);
+        if (elect_one()) tma_load_2d(sb + kXBytes + j * p.rank * kChunk * 2, &tmA, (c0 + c) * kChunk, row, full(s));
+        __syncwarp();
+      }
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issue (one elected lane)
@@ -211,58 +220,55 @@ lora_tile_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_cons
 namespace k14 {
 
 constexpr int kRows = kLoraTileRows;
-constexpr int kThreads = 192;                       // producer, MMA, four epilogue warps
+constexpr int kGroups = 2;                          // epilogue groups of four warps, taking pieces in turn
+constexpr int kUWarp0 = 2 + 4 * kGroups;
+constexpr int kThreads = (kUWarp0 + 4) * 32;        // producer, MMA, epilogue, U loaders
 constexpr int kMaxStages = 6;
-constexpr int kTmemCols = 256;                      // two accumulators of up to 128 columns
+constexpr int kBN = 128;                            // output columns per piece
+constexpr int kTmemU = kGroups * kBN;               // tensor memory: an accumulator per group, then two U
+constexpr int kTmemCols = 512;
+static_assert(kTmemU + 2 * kLoraMaxRank <= kTmemCols, "tensor memory");
 
 struct Params {
   const int32_t* tiles;
   const int32_t* requests;
-  const __nv_bfloat16* Yin;
+  const __nv_bfloat16* U;                           // kernel 13's
   __nv_bfloat16* Y;
   long long ldy;
   int ntiles;                                       // tiles with adapters; tiles after them are copied
-  int items, chunks;                                // (tile, BN columns) pieces; pieces per tile
-  int N, BN, rank, slots, adapters, stages;
-  int wu, wb;                                       // columns per box of U and of B: 64, 32 or 16
+  int items, chunks;                                // (tile, kBN columns) pieces; pieces per tile
+  int N, rank, slots, adapters, stages;
+  int wb;                                           // columns per box of B: 64, 32 or 16
   int early;                                        // y, B and the plan are complete before this grid's dependency
 };
 
-// Shared memory (1024-byte aligned): U | stages of (B, y) | barriers.
-struct Smem {
-  int u, b, y, stage, bar;
-};
-__host__ __device__ inline Smem smem_of(int jr, int BN, int stages) {
-  Smem m;
-  m.u = kRows * 2 * jr * 2;
-  m.b = BN * jr * 2;
-  m.y = kRows * BN * 2;
-  m.stage = m.b + m.y;
-  m.bar = m.u + stages * m.stage;
-  return m;
-}
-constexpr int kNumBars = 2 * kMaxStages + 7;        // full, empty, u_full, u_empty, acc_full[2], acc_empty[2], drain
-constexpr int smem_extra() { return 1024 + 8 * kNumBars + 16; }
+// Shared memory (1024-byte aligned): stages of (B, y) | barriers.
+__host__ __device__ constexpr int b_bytes(int jr) { return kBN * jr * 2; }
+__host__ __device__ constexpr int stage_bytes(int jr) { return b_bytes(jr) + kRows * kBN * 2; }
+constexpr int kNumBars = 2 * kMaxStages + 5 + 2 * kGroups;   // full, empty; u_full[2], u_empty[2], drain; acc_full, acc_empty
+constexpr int kSmemExtra = 1024 + 8 * kNumBars + 16;
 
-// Descriptor words of a K-major tile stored as boxes of w columns (128-, 64- or 32-byte swizzle).
+// Descriptor words of a K-major tile stored as boxes of w columns (128-, 64- or 32-byte swizzle).  All by
+// shifts: one thread issues the MMAs, and with divisions here (w is not known when compiling) 16 of them
+// took 3000 cycles.
 struct Boxes {
   uint32_t hi, box_bytes;
-  int w;
+  int lw;                                           // log2 w
 };
 __device__ __forceinline__ Boxes boxes(int w, int rows) {
   Boxes b;
-  b.w = w;
+  b.lw = w == 64 ? 6 : w == 32 ? 5 : 4;
   b.box_bytes = static_cast<uint32_t>(rows * w * 2);
   b.hi = w == 64 ? smem_desc_hi(1024, 2) : w == 32 ? smem_desc_hi(512, 4) : smem_desc_hi(256, 6);
   return b;
 }
-__device__ __forceinline__ uint64_t box_desc(const Boxes& b, uint32_t at, int col) {
-  return make_desc(((at + col / b.w * b.box_bytes + col % b.w * 2) >> 4) | (1u << 16), b.hi);
+__device__ __forceinline__ uint64_t box_desc(const Boxes& b, uint32_t at, uint32_t col) {
+  return make_desc(((at + (col >> b.lw) * b.box_bytes + (col & ((1u << b.lw) - 1)) * 2) >> 4) | (1u << 16), b.hi);
 }
 
 __global__ void __launch_bounds__(kThreads)
-lora_tile_up_kernel(const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmB,
-                    const __grid_constant__ CUtensorMap tmYin, const __grid_constant__ CUtensorMap tmY,
+lora_tile_up_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmYin,
+                    const __grid_constant__ CUtensorMap tmYin128, const __grid_constant__ CUtensorMap tmY,
                     const Params p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
@@ -270,15 +276,16 @@ lora_tile_up_kernel(const __grid_constant__ CUtensorMap tmU, const __grid_consta
   uint8_t* gbase = smem_raw + (base - raw);
   const int jr = p.slots * p.rank;
   const int S = p.stages;
-  const Smem sm = smem_of(jr, p.BN, S);
-  const uint32_t bars = base + sm.bar;
+  const int stage = stage_bytes(jr);
+  const uint32_t bars = base + S * stage;
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (kMaxStages + s); };
-  const uint32_t u_full = bars + 8u * (2 * kMaxStages), u_empty = u_full + 8u;
-  auto acc_full = [&](int b) { return u_full + 16u + 8u * b; };
-  auto acc_empty = [&](int b) { return u_full + 32u + 8u * b; };
-  const uint32_t drain = u_full + 48u;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + sm.bar + 8 * kNumBars);
+  auto u_full = [&](int u) { return bars + 8u * (2 * kMaxStages + u); };
+  auto u_empty = [&](int u) { return bars + 8u * (2 * kMaxStages + 2 + u); };
+  auto acc_full = [&](int b) { return bars + 8u * (2 * kMaxStages + 4 + b); };
+  auto acc_empty = [&](int b) { return bars + 8u * (2 * kMaxStages + 4 + kGroups + b); };
+  const uint32_t drain = bars + 8u * (2 * kMaxStages + 4 + 2 * kGroups);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + S * stage + 8 * kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -287,15 +294,14 @@ lora_tile_up_kernel(const __grid_constant__ CUtensorMap tmU, const __grid_consta
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < S; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 5); }   // four epilogue warps, the MMAs
-    mbar_init(u_full, 1);
-    mbar_init(u_empty, 1);
-    for (int b = 0; b < 2; ++b) { mbar_init(acc_full(b), 1); mbar_init(acc_empty(b), 4); }
+    for (int u = 0; u < 2; ++u) { mbar_init(u_full(u), 4); mbar_init(u_empty(u), 1); }
+    for (int b = 0; b < kGroups; ++b) { mbar_init(acc_full(b), 1); mbar_init(acc_empty(b), 4); }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    prefetch_tmap(&tmU);
     prefetch_tmap(&tmB);
     prefetch_tmap(&tmYin);
+    prefetch_tmap(&tmYin128);
     prefetch_tmap(&tmY);
   }
   if (warp == 1) tmem_alloc<kTmemCols>(smem_addr(tmem_slot));
@@ -310,56 +316,49 @@ lora_tile_up_kernel(const __grid_constant__ CUtensorMap tmU, const __grid_consta
     // ---------------------------------------------------------------- TMA producer
     // With early, y, B and the plan are older than kernel 13 (which let this grid start after its own
     // dependency wait): their loads go out at once, and only U waits for kernel 13.
-    bool waited = !p.early;
-    int last = -1, it = 0, nu = 0;
+    int last = -1, it = 0;
+    int4 tile = make_int4(0, 0, 0, 0);
+    int b_row = 0;                                  // lane j: first row of slot j's adapter in B
     for (int i = i0; i < i1; ++i, ++it) {
-      const int t = i / p.chunks, n0 = i % p.chunks * p.BN;
+      const int t = i / p.chunks, n0 = i % p.chunks * kBN;
       const int s = it % S;
-      const int4 tile = tile_of(t);
       const bool busy = t < p.ntiles;
-      const bool new_u = busy && t != last;
+      if (t != last) {                              // the plan is read once per tile, not per piece
+        tile = tile_of(t);
+        if (busy && lane < p.slots) {
+          const int id = __ldcg(p.requests + static_cast<size_t>(tile.z) * 2 * p.slots + lane);
+          b_row = id < 0 ? -1 : id * p.N;
+        }
+        last = t;
+      }
       if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty(s), ((it / S) & 1u) ^ 1u, abort_flag, 81))) break;
+      const int slabs = (tile.y + 31) / 32, halves = min(kBN, p.N - n0) / 64;
+      const uint32_t sb = base + s * stage;
       if (elect_one()) {
-        const int slabs = (tile.y + 31) / 32, halves = min(p.BN, p.N - n0) / 64;
-        const uint32_t sb = base + sm.u + s * sm.stage;
-        mbar_arrive_expect_tx(full(s), slabs * halves * 4096 + (busy ? sm.b : 0));
-        for (int h = 0; h < halves; ++h)
-          for (int q = 0; q < slabs; ++q)
-            tma_load_2d(sb + sm.b + (h * 4 + q) * 4096, &tmYin, n0 + 64 * h, tile.x + 32 * q, full(s));
-        if (busy) {
-          const int32_t* req = p.requests + static_cast<size_t>(tile.z) * 2 * p.slots;
-          uint32_t at = sb;
-          for (int j = 0; j < p.slots; ++j) {
-            const int id = __ldcg(req + j);         // an empty slot's rows lie past the pool: read as zeros
-            for (int c = 0; c < p.rank; c += p.wb, at += p.BN * p.wb * 2)
-              tma_load_2d(at, &tmB, c, id < 0 ? p.adapters * p.N : id * p.N + n0, full(s));
+        mbar_arrive_expect_tx(full(s), slabs * halves * 4096 + (busy ? b_bytes(jr) : 0));
+        for (int h = 0; h < halves; ++h) {
+          if (slabs == 4) {                         // one box of 128 rows
+            tma_load_2d(sb + b_bytes(jr) + h * 16384, &tmYin128, n0 + 64 * h, tile.x, full(s));
+            continue;
           }
+          for (int q = 0; q < slabs; ++q)
+            tma_load_2d(sb + b_bytes(jr) + (h * 4 + q) * 4096, &tmYin, n0 + 64 * h, tile.x + 32 * q, full(s));
         }
       }
       __syncwarp();
-      if (new_u) {
-        if (!waited) {
-          grid_dependency_wait();
-          waited = true;
-        }
-        // the previous tile's MMAs have read U
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(u_empty, (nu & 1u) ^ 1u, abort_flag, 82))) break;
-        if (elect_one()) {
-          mbar_arrive_expect_tx(u_full, sm.u);
-          for (int c = 0; c < 2 * jr; c += p.wu)
-            tma_load_2d(base + c * kRows * 2, &tmU, c, t * kRows, u_full);
-        }
+      for (int j = 0; busy && j < p.slots; ++j) {   // an empty slot's rows lie past the pool: read as zeros
+        const int row = __shfl_sync(0xFFFFFFFFu, b_row, j);
+        if (elect_one())
+          for (int c = 0; c < p.rank; c += p.wb)
+            tma_load_2d(sb + (j * p.rank + c) * kBN * 2, &tmB, c, row < 0 ? p.adapters * p.N : row + n0, full(s));
         __syncwarp();
-        last = t;
-        ++nu;
       }
     }
-    if (!waited) grid_dependency_wait();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issue (one elected lane)
-    const uint32_t idesc = k13::idesc_bf16(p.BN);
-    const Boxes bu = boxes(p.wu, kRows), bb = boxes(p.wb, p.BN);
-    int last = -1, it = 0, nu = 0, na = 0;
+    const uint32_t idesc = k13::idesc_bf16(kBN);
+    const Boxes bb = boxes(p.wb, kBN);
+    int last = -1, it = 0, nu = 0;                  // nu: tiles begun
     for (int i = i0; i < i1; ++i, ++it) {
       const int t = i / p.chunks;
       const int s = it % S;
@@ -368,55 +367,87 @@ lora_tile_up_kernel(const __grid_constant__ CUtensorMap tmU, const __grid_consta
         if (lane == 0) mbar_arrive(empty(s));
         continue;
       }
-      const int b = na & 1;
+      const int b = it % kGroups;                   // copied pieces come last, so this counts MMA pieces
       bool ok = true;
       if (t != last) {
-        ok = mbar_wait_bounded(u_full, nu & 1u, abort_flag, 84);
+        ok = mbar_wait_bounded(u_full(nu & 1), (nu >> 1) & 1u, abort_flag, 84);
         last = t;
         ++nu;
       }
       ok = ok && mbar_wait_bounded(full(s), (it / S) & 1u, abort_flag, 85);
-      ok = ok && mbar_wait_bounded(acc_empty(b), ((na >> 1) & 1u) ^ 1u, abort_flag, 86);
+      ok = ok && mbar_wait_bounded(acc_empty(b), ((it / kGroups) & 1u) ^ 1u, abort_flag, 86);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc_fence_after();
       if (elect_one()) {
-        const uint32_t sb = base + sm.u + s * sm.stage;
-        for (int c = 0; c < 2 * jr; c += 16)
-          umma_bf16(tmem + static_cast<uint32_t>(b * 128), box_desc(bu, base, c), box_desc(bb, sb, c < jr ? c : c - jr),
-                    idesc, c != 0 ? 1u : 0u);
+        const uint32_t sb = base + s * stage;
+        const uint32_t d = tmem + static_cast<uint32_t>(b * kBN);
+        const uint32_t u = tmem + static_cast<uint32_t>(kTmemU + ((nu - 1) & 1) * kLoraMaxRank);
+#pragma unroll 2
+        for (int c = 0; c < jr; c += 16) {          // hi and lo against the same columns of B
+          const uint64_t db = box_desc(bb, sb, c);
+          umma_bf16_ta(d, u + c / 2, db, idesc, c != 0 ? 1u : 0u);
+          umma_bf16_ta(d, u + (jr + c) / 2, db, idesc, 1u);
+        }
         tc_commit(acc_full(b));
         tc_commit(empty(s));
-        if (i + 1 == i1 || (i + 1) / p.chunks != t) tc_commit(u_empty);
+        if (i + 1 == i1 || (i + 1) / p.chunks != t) tc_commit(u_empty((nu - 1) & 1));
       }
       __syncwarp();
-      ++na;
+    }
+  } else if (warp >= kUWarp0) {
+    // ---------------------------------------------------------------- U loaders: a row per thread
+    if (p.early) grid_dependency_wait();            // kernel 13 is done
+    const int q = warp & 3;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(kTmemU);
+    int nu = 0;
+    for (int t = i0 / p.chunks; t < p.ntiles && t * static_cast<long long>(p.chunks) < i1; ++t, ++nu) {
+      const uint4* src = reinterpret_cast<const uint4*>(p.U + (static_cast<size_t>(t) * kRows + q * 32 + lane) * (2 * jr));
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(u_empty(nu & 1), ((nu >> 1) & 1u) ^ 1u, abort_flag, 82))) break;
+      tc_fence_after();
+#pragma unroll 2
+      for (int c = 0; c < jr; c += 16) {            // 16 words = 32 values
+        uint32_t v[16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 w = __ldcg(src + c / 4 + j);
+          v[4 * j] = w.x;
+          v[4 * j + 1] = w.y;
+          v[4 * j + 2] = w.z;
+          v[4 * j + 3] = w.w;
+        }
+        tmem_st_32x32b_x16(trow + static_cast<uint32_t>((nu & 1) * kLoraMaxRank + c), v);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(u_full(nu & 1));
     }
   } else {
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3;                         // tensor-memory lane quarter = 32-row slab of the tile
-    const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const int b = (warp - 2) / 4;                   // group, and its accumulator
+    const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(b * kBN);
     const uint32_t sw = static_cast<uint32_t>(lane & 7);
-    int it = 0, na = 0, held = -1;                  // held: the stage whose store is still being read out
-    for (int i = i0; i < i1; ++i, ++it) {
-      const int t = i / p.chunks, n0 = i % p.chunks * p.BN;
+    int last = -1;
+    int4 tile = make_int4(0, 0, 0, 0);
+    for (int it = b; i0 + it < i1; it += kGroups) {
+      const int i = i0 + it;
+      const int t = i / p.chunks, n0 = i % p.chunks * kBN;
       const int s = it % S;
-      const int4 tile = tile_of(t);
+      if (t != last) tile = tile_of(t);
+      last = t;
       const bool busy = t < p.ntiles;
-      const int b = na & 1;
       bool ok = mbar_wait_bounded(full(s), (it / S) & 1u, abort_flag, 87);
-      if (busy) {
-        ok = ok && mbar_wait_bounded(acc_full(b), (na >> 1) & 1u, abort_flag, 88);
-        ++na;
-      }
+      if (busy) ok = ok && mbar_wait_bounded(acc_full(b), (it / kGroups) & 1u, abort_flag, 88);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc_fence_after();
       const int rows = min(32, tile.y - 32 * q);    // of this slab; none or fewer where the tile ends
-      const int halves = min(p.BN, p.N - n0) / 64;
-      const uint32_t yq = base + sm.u + s * sm.stage + sm.b + q * 4096;
+      const int halves = min(kBN, p.N - n0) / 64;
+      const uint32_t yq = base + s * stage + b_bytes(jr) + q * 4096;
       if (rows > 0 && busy) {
         for (int h = 0; h < 2 * halves; ++h) {      // 32 columns at a time
           uint32_t v[32];
-          tmem_ld_32x32b_x32(trow + static_cast<uint32_t>(b * 128 + 32 * h), v);
+          tmem_ld_32x32b_x32(trow + static_cast<uint32_t>(32 * h), v);
           const uint32_t yrow = yq + (h >> 1) * 16384 + lane * 128;
           uint4 y[4];
 #pragma unroll
@@ -461,20 +492,14 @@ lora_tile_up_kernel(const __grid_constant__ CUtensorMap tmU, const __grid_consta
             *reinterpret_cast<uint4*>(p.Y + (tile.x + 32 * q + r) * p.ldy + n0 + 64 * h + 8 * c) = v;
           }
       }
-      // hand the previous piece's stage back once its store has read it
-      if (lane == 0) {
+      if (lane == 0) {                              // hand the stage back once its store has read it
         bulk_commit_group();
-        bulk_wait_group_read<1>();
-        if (held >= 0) mbar_arrive(empty(held));
+        bulk_wait_group_read<0>();
+        mbar_arrive(empty(s));
       }
-      held = s;
       __syncwarp();
     }
-    if (lane == 0) {
-      bulk_wait_group_read<0>();
-      if (held >= 0) mbar_arrive(empty(held));
-      bulk_wait_group<0>();
-    }
+    if (lane == 0) bulk_wait_group<0>();
     __syncwarp();
   }
   grid_launch_dependents();
