@@ -20,22 +20,23 @@ bool sizes_ok(int M, int requests, int slots) {
 
 size_t tiles_of(size_t rows) { return (rows + kLoraTileRows - 1) / kLoraTileRows; }
 
-// What a plan holds, counted or written (out null: counted only).
+// What a plan holds.
 struct Pack {
   const int32_t* off;
   const int32_t* ids;
   const float* w;
   int requests, slots, M;
   std::vector<int> shorts;                 // short requests, ordered by their adapter ids
-  size_t tiles = 0, copies = 0, groups = 0;
+  size_t tiles = 0, copy_tiles = 0, groups = 0, copy_groups = 0;
 
+  const int32_t* ids_of(int r) const { return ids + static_cast<size_t>(r) * slots; }
+  const float* w_of(int r) const { return w + static_cast<size_t>(r) * slots; }
   bool has_adapter(int r) const {
     for (int j = 0; j < slots; ++j)
-      if (ids[static_cast<size_t>(r) * slots + j] >= 0) return true;
+      if (ids_of(r)[j] >= 0) return true;
     return false;
   }
   int rows(int r) const { return off[r + 1] - off[r]; }
-  bool is_short(int r) const { return rows(r) <= svdq::kLoraShortRows; }
 
   // runs of rows that no adapter touches: f(first row, rows)
   template <class F>
@@ -49,14 +50,17 @@ struct Pack {
     if (M > from) f(from, M - from);
   }
 
+  // Untouched runs become copy tiles, or rows of copy groups where they are short and kernel 14 is not
+  // launched for long requests anyway.
+  bool copied_as_rows(int n) const { return tiles == 0 && n <= svdq::kLoraShortRows; }
+
   int compare_ids(int a, int b) const {
-    const int32_t *x = ids + static_cast<size_t>(a) * slots, *y = ids + static_cast<size_t>(b) * slots;
     for (int j = 0; j < slots; ++j)
-      if (x[j] != y[j]) return x[j] < y[j] ? -1 : 1;
+      if (ids_of(a)[j] != ids_of(b)[j]) return ids_of(a)[j] < ids_of(b)[j] ? -1 : 1;
     return 0;
   }
 
-  // groups of at most kLoraGroupRows rows of short requests with the same ids, in order:
+  // rows of short requests, those with the same ids together, in groups of at most kLoraGroupRows:
   // f(request, row, first of its group)
   template <class F>
   void grouped(F f) const {
@@ -74,48 +78,57 @@ struct Pack {
   void count() {
     for (int r = 0; r < requests; ++r) {
       if (rows(r) == 0 || !has_adapter(r)) continue;
-      if (is_short(r)) shorts.push_back(r);
+      if (rows(r) <= svdq::kLoraShortRows) shorts.push_back(r);
       else tiles += tiles_of(rows(r));
     }
     std::stable_sort(shorts.begin(), shorts.end(), [&](int a, int b) { return compare_ids(a, b) < 0; });
-    untouched([&](int, int n) { copies += tiles_of(n); });
     grouped([&](int, int, bool first) { groups += first; });
+    size_t few = 0;
+    untouched([&](int, int n) {
+      if (copied_as_rows(n)) few += n;
+      else copy_tiles += tiles_of(n);
+    });
+    copy_groups = (few + kLoraGroupRows - 1) / kLoraGroupRows;
   }
 
   void write(int32_t* out, int adapters) const {
-    const svdq::LoraLayout L = svdq::lora_layout(requests, slots, tiles + copies, groups);
+    const svdq::LoraLayout L = svdq::lora_layout(slots, tiles + copy_tiles, groups + copy_groups);
     memset(out, 0, L.words * sizeof(int32_t));
     memcpy(out, "SVDQLORA", 8);
-    const int32_t head[7] = {M, requests, slots, adapters, static_cast<int32_t>(tiles), static_cast<int32_t>(copies),
-                             static_cast<int32_t>(groups)};
+    const int32_t head[8] = {M, requests, slots, adapters, static_cast<int32_t>(tiles),
+                             static_cast<int32_t>(copy_tiles), static_cast<int32_t>(groups),
+                             static_cast<int32_t>(copy_groups)};
     memcpy(out + 2, head, sizeof(head));
-    for (int r = 0; r < requests; ++r) {
-      int32_t* q = out + L.requests + static_cast<size_t>(r) * 2 * slots;
-      memcpy(q, ids + static_cast<size_t>(r) * slots, slots * sizeof(int32_t));
-      memcpy(q + slots, w + static_cast<size_t>(r) * slots, slots * sizeof(float));
-    }
+    const std::vector<int32_t> none(slots, -1);
     int32_t* t = out + L.tiles;
-    auto put = [&](int row, int n, int r) {
-      for (; n > 0; row += kLoraTileRows, n -= kLoraTileRows, t += 4) {
+    auto put_tiles = [&](int row, int n, int r) {
+      for (; n > 0; row += kLoraTileRows, n -= kLoraTileRows, t += svdq::lora_tile_words(slots)) {
         t[0] = row;
         t[1] = std::min(n, kLoraTileRows);
         t[2] = r;
+        memcpy(t + 4, r < 0 ? none.data() : ids_of(r), slots * sizeof(int32_t));
+        if (r >= 0) memcpy(t + 4 + slots, w_of(r), slots * sizeof(float));
       }
     };
     for (int r = 0; r < requests; ++r)
-      if (rows(r) > 0 && has_adapter(r) && !is_short(r)) put(off[r], rows(r), r);
-    untouched([&](int row, int n) { put(row, n, -1); });
+      if (rows(r) > svdq::kLoraShortRows && has_adapter(r)) put_tiles(off[r], rows(r), r);
     int32_t* g = nullptr;
     int32_t* next = out + L.groups;
-    grouped([&](int r, int m, bool first) {
+    auto put_row = [&](int m, int r, bool first) {
       if (first) {
         g = next;
         next += svdq::lora_group_words(slots);
-        for (int j = 0; j < 8; ++j) g[4 + j] = j < slots ? ids[static_cast<size_t>(r) * slots + j] : -1;
+        for (int j = 0; j < 8; ++j) g[4 + j] = j < slots && r >= 0 ? ids_of(r)[j] : -1;
       }
       const int i = g[0]++;
       g[12 + i] = m;
-      memcpy(g + 12 + kLoraGroupRows + i * slots, w + static_cast<size_t>(r) * slots, slots * sizeof(float));
+      if (r >= 0) memcpy(g + 12 + kLoraGroupRows + i * slots, w_of(r), slots * sizeof(float));
+    };
+    grouped([&](int r, int m, bool first) { put_row(m, r, first); });
+    int held = 0;
+    untouched([&](int row, int n) {
+      if (!copied_as_rows(n)) return put_tiles(row, n, -1);
+      for (int m = row; m < row + n; ++m, held = (held + 1) % kLoraGroupRows) put_row(m, -1, held == 0);
     });
   }
 };
@@ -129,8 +142,8 @@ size_t svdq_lora_plan_bytes(int M, int requests, int slots) {
   const size_t r = static_cast<size_t>(requests), m = static_cast<size_t>(M);
   // every request, and every run of rows between requests, ends in a tile or group that may not be full
   const size_t tiles = 2 * (m / kLoraTileRows + r + 1);
-  const size_t groups = m / kLoraGroupRows + r;
-  return svdq::lora_layout(r, slots, tiles, groups).words * sizeof(int32_t);
+  const size_t groups = m / kLoraGroupRows + r + 1;
+  return svdq::lora_layout(slots, tiles, groups).words * sizeof(int32_t);
 }
 
 int svdq_lora_plan_pack(const int32_t* row_offsets, const int32_t* adapter_ids, const float* weights, int requests,
@@ -146,12 +159,12 @@ int svdq_lora_plan_pack(const int32_t* row_offsets, const int32_t* adapter_ids, 
   try {
     Pack p{row_offsets, adapter_ids, weights, requests, slots, M, {}};
     p.count();
-    const svdq::LoraLayout L = svdq::lora_layout(requests, slots, p.tiles + p.copies, p.groups);
+    const svdq::LoraLayout L = svdq::lora_layout(slots, p.tiles + p.copy_tiles, p.groups + p.copy_groups);
     if (out_bytes < L.words * sizeof(int32_t)) return SVDQ_ERR_INVALID_ARG;
     p.write(static_cast<int32_t*>(out), adapters);
     *plan = svdq_lora_plan{M, requests, slots, adapters, static_cast<int32_t>(p.tiles),
-                           static_cast<int32_t>(p.copies), static_cast<int32_t>(p.groups), 0};
-    plan->bytes = static_cast<int64_t>(L.words * sizeof(int32_t));
+                           static_cast<int32_t>(p.copy_tiles), static_cast<int32_t>(p.groups),
+                           static_cast<int32_t>(p.copy_groups), static_cast<int64_t>(L.words * sizeof(int32_t))};
   } catch (...) {                          // no memory for the host's lists
     return SVDQ_ERR_INVALID_ARG;
   }

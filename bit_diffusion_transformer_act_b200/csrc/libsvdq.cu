@@ -892,10 +892,9 @@ static int lora_short_splits(int groups, int K, int jr, int dev) {
 
 static bool lora_plan_ok(const svdq_lora_plan* p) {
   return p && p->M >= 0 && p->requests >= 0 && p->slots >= 1 && p->slots <= svdq::kLoraMaxSlots && p->adapters >= 0 &&
-         p->tiles >= 0 && p->copy_tiles >= 0 && p->groups >= 0 &&
-         p->bytes == static_cast<int64_t>(4 * svdq::lora_layout(p->requests, p->slots,
-                                                                static_cast<size_t>(p->tiles) + p->copy_tiles,
-                                                                p->groups).words);
+         p->tiles >= 0 && p->copy_tiles >= 0 && p->groups >= 0 && p->copy_groups >= 0 &&
+         p->bytes == static_cast<int64_t>(4 * svdq::lora_layout(p->slots, static_cast<size_t>(p->tiles) + p->copy_tiles,
+                                                                static_cast<size_t>(p->groups) + p->copy_groups).words);
 }
 
 // The workspace: kernel 13's U, then kernel 11's parts.
@@ -931,7 +930,7 @@ struct LoraCall {
   void *Y, *ws, *stream;
   int64_t ldx, ldyin, ldy;
   const svdq_lora_plan* plan;
-  const int32_t *requests, *tiles, *groups;         // the plan's sections on the device
+  const int32_t *tiles, *groups;                    // the plan's sections on the device
   int M, N, K, rank, jr, dev;
 };
 
@@ -946,7 +945,6 @@ static int lora_tiles_launch(const LoraCall& c, bool copy) {
   if (tiles > 0) {
     k13::Params p;
     p.tiles = c.tiles;
-    p.requests = c.requests;
     p.U = static_cast<__nv_bfloat16*>(c.ws);
     p.K = c.K;
     p.rank = c.rank;
@@ -970,7 +968,6 @@ static int lora_tiles_launch(const LoraCall& c, bool copy) {
   }
   k14::Params p;
   p.tiles = c.tiles;
-  p.requests = c.requests;
   p.U = static_cast<const __nv_bfloat16*>(c.ws);
   p.Y = static_cast<__nv_bfloat16*>(c.Y);
   p.ldy = c.ldy;
@@ -1003,8 +1000,8 @@ static int lora_tiles_launch(const LoraCall& c, bool copy) {
   return SVDQ_OK;
 }
 
-// Kernels 11 and 12: the groups of short requests.
-static int lora_groups_launch(const LoraCall& c, float* part) {
+// Kernels 11 and 12: the groups of short requests, and (copy) of the rows to copy.
+static int lora_groups_launch(const LoraCall& c, bool copy, float* part) {
   namespace k11 = svdq::k11;
   k11::Params p;
   p.X = static_cast<const __nv_bfloat16*>(c.X);
@@ -1021,14 +1018,42 @@ static int lora_groups_launch(const LoraCall& c, float* part) {
   p.K = c.K;
   p.rank = c.rank;
   p.slots = c.plan->slots;
-  p.ks = lora_short_splits(c.plan->groups, c.K, c.jr, c.dev);
-  if (!launch_pdl(k11::lora_short_down_kernel, dim3(c.plan->groups, c.jr / 16, p.ks), k11::kThreads, 0, 1, c.stream, p))
-    return SVDQ_ERR_CUDA;
+  p.ngroups = c.plan->groups;
+  p.early = p.ngroups > 0;
+  p.ks = 1;
+  if (p.ngroups > 0) {
+    p.ks = lora_short_splits(p.ngroups, c.K, c.jr, c.dev);
+    if (!launch_pdl(k11::lora_short_down_kernel, dim3(p.ngroups, c.jr / 16, p.ks), k11::kThreads, 0, 1, c.stream, p))
+      return SVDQ_ERR_CUDA;
+  }
+  const int all = p.ngroups + (copy ? c.plan->copy_groups : 0);
   const int strips = (c.N / 16 + k11::kWarps - 1) / k11::kWarps;
-  const int ny = std::max(1, std::min(strips, 8 * sm_count(c.dev) / c.plan->groups));
-  if (!launch_pdl(k11::lora_short_up_kernel, dim3(c.plan->groups, ny), k11::kThreads, 0, 1, c.stream, p))
-    return SVDQ_ERR_CUDA;
-  return SVDQ_OK;
+  const dim3 grid(all, std::max(1, std::min(strips, 4 * sm_count(c.dev) / all)));
+#define SVDQ_LORA_UP(WIDE_, STEPS_)                                                                              \
+  case STEPS_:                                                                                                   \
+    return launch_pdl(k11::lora_short_up_kernel<WIDE_, STEPS_>, grid, k11::kThreads, 0, 1, c.stream, p) ? SVDQ_OK \
+                                                                                                         : SVDQ_ERR_CUDA
+  if (c.rank % 32 == 0) {
+    switch (c.jr / 32) {
+      SVDQ_LORA_UP(true, 1);
+      SVDQ_LORA_UP(true, 2);
+      SVDQ_LORA_UP(true, 3);
+      SVDQ_LORA_UP(true, 4);
+    }
+  } else {
+    switch (c.jr / 16) {
+      SVDQ_LORA_UP(false, 1);
+      SVDQ_LORA_UP(false, 2);
+      SVDQ_LORA_UP(false, 3);
+      SVDQ_LORA_UP(false, 4);
+      SVDQ_LORA_UP(false, 5);
+      SVDQ_LORA_UP(false, 6);
+      SVDQ_LORA_UP(false, 7);
+      SVDQ_LORA_UP(false, 8);
+    }
+  }
+#undef SVDQ_LORA_UP
+  return SVDQ_ERR_UNSUPPORTED_SHAPE;
 }
 
 int svdq_lora_add(const void* X, int64_t ldx, const void* Yin, int64_t ldyin, const void* A, const void* B,
@@ -1060,14 +1085,15 @@ int svdq_lora_add(const void* X, int64_t ldx, const void* Yin, int64_t ldyin, co
   const LoraWorkspace ws = lora_workspace(plan, K, plan->slots * rank, dev);
   if (work && workspace_bytes < ws.total) return SVDQ_ERR_INVALID_ARG;
 
-  const svdq::LoraLayout L = svdq::lora_layout(plan->requests, plan->slots, all_tiles, plan->groups);
+  const svdq::LoraLayout L = svdq::lora_layout(plan->slots, all_tiles, static_cast<size_t>(plan->groups) + plan->copy_groups);
   const int32_t* words = static_cast<const int32_t*>(plan_dev);
-  const LoraCall c{X,   Yin, A,     B,    Y, workspace, stream, ldx,  ldyin,
-                   ldy, plan, words + L.requests, words + L.tiles, words + L.groups, M, N, K, rank, plan->slots * rank, dev};
+  const LoraCall c{X,    Yin, A, B, Y, workspace, stream, ldx, ldyin, ldy, plan, words + L.tiles, words + L.groups, M, N, K,
+                   rank, plan->slots * rank, dev};
   if (plan->tiles > 0 || (plan->copy_tiles > 0 && !in_place))
     if (int st = lora_tiles_launch(c, !in_place)) return st;
-  if (plan->groups > 0)
-    if (int st = lora_groups_launch(c, reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ws.part))) return st;
+  if (plan->groups > 0 || (plan->copy_groups > 0 && !in_place))
+    if (int st = lora_groups_launch(c, !in_place, reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ws.part)))
+      return st;
   return launch_status();
 }
 

@@ -31,6 +31,8 @@ struct Params {
   const int32_t* groups;                   // the plan's group records
   float* part;                             // [groups][ks][16 rows][slots rank]
   int N, K, rank, slots, ks;
+  int ngroups;                             // groups with adapters; groups after them are copied
+  int early;                               // kernel 12: kernel 11 comes before it
 };
 
 // D (16 x 8, fp32) += A (16 x 16) B (16 x 8), bf16: lane (g = lane / 4, t = lane % 4) holds rows g and
@@ -107,22 +109,79 @@ lora_short_down_kernel(const Params p) {
 
 constexpr int kUStride = kLoraMaxRank + 8;         // bf16 per row of u in shared memory
 
+// kWide: 32 ranks per step, a lane's share of a row of B one 16-byte load (rank % 32 == 0); else 16 and an
+// 8-byte load.  kSteps = slots rank / (32 or 16).  A warp's next 16 columns of B and y are in flight while it
+// works on the present ones, and the first are requested before the grid's dependency: kernel 11 lets this
+// grid start after its own dependency wait, so B, y and the plan are complete by then.
+template <bool kWide, int kSteps>
 __global__ void __launch_bounds__(kThreads)
 lora_short_up_kernel(const Params p) {
+  constexpr int kSpan = kWide ? 32 : 16;           // ranks per step
+  constexpr int kWords = kWide ? 4 : 2;            // 32-bit words of a row of B per lane and step
   __shared__ __align__(16) uint16_t uh[G * kUStride], ul[G * kUStride];
   __shared__ __align__(16) float ds[kWarps][G][20];
+  __shared__ int32_t head[4 + 8 + G];              // the record's rows, ids and row indexes
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  grid_dependency_wait();                          // the parts of u, and y
-  grid_launch_dependents();
   const int32_t* rec = p.groups + static_cast<size_t>(blockIdx.x) * lora_group_words(p.slots);
-  const int nrows = rec[0];
+  if (!p.early) grid_dependency_wait();
+  if (threadIdx.x < 4 + 8 + G) head[threadIdx.x] = __ldcg(rec + threadIdx.x);
+  __syncthreads();
+  const int nrows = head[0];
   const int jr = p.slots * p.rank;
+  const int step_n = gridDim.y * kWarps * 16;
+  const int yi = lane / 2, yc = 8 * (lane % 2);    // this lane's row of the group and columns of y
+  const long long yrow = yi < nrows ? head[12 + yi] : 0;
+
+  const bool copied = static_cast<int>(blockIdx.x) >= p.ngroups;   // rows that no adapter touches
+  const uint32_t* brow[kSteps];                    // this lane's words of row g of each step's block of B
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const int id = copied ? -1 : head[4 + s * kSpan / p.rank];
+    brow[s] = id < 0 ? nullptr
+                     : reinterpret_cast<const uint32_t*>(p.B + (static_cast<size_t>(id) * p.N + g) * p.rank +
+                                                         s * kSpan % p.rank + kSpan / 4 * t);
+  }
+  uint32_t bl[kSteps][kWords], bh[kSteps][kWords]; // rows n0 + g and n0 + g + 8
+  uint4 y = make_uint4(0u, 0u, 0u, 0u);
+  auto fetch = [&](int n0) {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      if (!brow[s]) {
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) bl[s][w] = bh[s][w] = 0u;
+        continue;
+      }
+      const uint32_t* lo = brow[s] + static_cast<size_t>(n0) * p.rank / 2;
+      const uint32_t* hi = lo + 4 * p.rank;
+      if constexpr (kWide) {
+        const uint4 a = __ldcg(reinterpret_cast<const uint4*>(lo)), b = __ldcg(reinterpret_cast<const uint4*>(hi));
+        bl[s][0] = a.x; bl[s][1] = a.y; bl[s][2] = a.z; bl[s][3] = a.w;
+        bh[s][0] = b.x; bh[s][1] = b.y; bh[s][2] = b.z; bh[s][3] = b.w;
+      } else {
+        const uint2 a = __ldcg(reinterpret_cast<const uint2*>(lo)), b = __ldcg(reinterpret_cast<const uint2*>(hi));
+        bl[s][0] = a.x; bl[s][1] = a.y;
+        bh[s][0] = b.x; bh[s][1] = b.y;
+      }
+    }
+    if (yi < nrows) y = __ldcg(reinterpret_cast<const uint4*>(p.Yin + yrow * p.ldyin + n0 + yc));
+  };
+  int n0 = (blockIdx.y * kWarps + warp) * 16;
+  if (n0 < p.N) fetch(n0);
+  if (p.early) grid_dependency_wait();             // the parts of u
+  grid_launch_dependents();
+  if (copied) {
+    for (; n0 < p.N; n0 += step_n) {
+      if (yi < nrows) *reinterpret_cast<uint4*>(p.Y + yrow * p.ldy + n0 + yc) = y;
+      if (n0 + step_n < p.N) fetch(n0 + step_n);
+    }
+    return;
+  }
   for (int i = threadIdx.x; i < G * jr; i += kThreads) {
     const int row = i / jr, c = i % jr;
     float u = 0.f;
     if (row < nrows) {
       const float* src = p.part + (static_cast<size_t>(blockIdx.x) * p.ks * G + row) * jr + c;
-      for (int z = 0; z < p.ks; ++z) u += src[static_cast<size_t>(z) * G * jr];
+      for (int z = 0; z < p.ks; ++z) u += __ldcg(src + static_cast<size_t>(z) * G * jr);
     }
     float lo;
     uh[row * kUStride + c] = split_hi_lo(u, lo);
@@ -130,28 +189,25 @@ lora_short_up_kernel(const Params p) {
   }
   __syncthreads();
   const int nt = nrows > 8 ? 2 : 1;
-  for (int n0 = (blockIdx.y * kWarps + warp) * 16; n0 < p.N; n0 += gridDim.y * kWarps * 16) {
+  for (; n0 < p.N; n0 += step_n) {
     float d[2][4] = {};
-    for (int j = 0; j < p.slots; ++j) {
-      const int id = rec[4 + j];
-      if (id < 0) continue;
-      const __nv_bfloat16* b_lo = p.B + (static_cast<size_t>(id) * p.N + n0 + g) * p.rank + 4 * t;
-      const __nv_bfloat16* b_hi = b_lo + 8 * p.rank;
-#pragma unroll 4
-      for (int s = 0; s < p.rank / 16; ++s) {
-        const uint2 lo = __ldg(reinterpret_cast<const uint2*>(b_lo + 16 * s));
-        const uint2 hi = __ldg(reinterpret_cast<const uint2*>(b_hi + 16 * s));
-        const int c = j * p.rank + 16 * s + 4 * t;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h >= nt) continue;
-          const uint2 vh = *reinterpret_cast<const uint2*>(uh + (8 * h + g) * kUStride + c);
-          const uint2 vl = *reinterpret_cast<const uint2*>(ul + (8 * h + g) * kUStride + c);
-          mma16816(d[h], lo.x, hi.x, lo.y, hi.y, vh.x, vh.y);
-          mma16816(d[h], lo.x, hi.x, lo.y, hi.y, vl.x, vl.y);
+    for (int s = 0; s < kSteps; ++s) {
+      const int c = s * kSpan + kSpan / 4 * t;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h >= nt) continue;
+#pragma unroll
+        for (int w = 0; w < kWords; w += 2) {
+          const uint2 vh = *reinterpret_cast<const uint2*>(uh + (8 * h + g) * kUStride + c + 2 * w);
+          const uint2 vl = *reinterpret_cast<const uint2*>(ul + (8 * h + g) * kUStride + c + 2 * w);
+          mma16816(d[h], bl[s][w], bh[s][w], bl[s][w + 1], bh[s][w + 1], vh.x, vh.y);
+          mma16816(d[h], bl[s][w], bh[s][w], bl[s][w + 1], bh[s][w + 1], vl.x, vl.y);
         }
       }
     }
+    const uint4 yv = y;
+    if (n0 + step_n < p.N) fetch(n0 + step_n);
     // through shared memory: a lane adds 8 columns of one row
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -161,18 +217,15 @@ lora_short_up_kernel(const Params p) {
       ds[warp][8 * h + 2 * t + 1][g + 8] = d[h][3];
     }
     __syncwarp();
-    const int i = lane / 2, c = 8 * (lane % 2);
-    if (i < nrows) {
-      const long long row = rec[12 + i];
-      const uint4 y = *reinterpret_cast<const uint4*>(p.Yin + row * p.ldyin + n0 + c);
-      const float* v = &ds[warp][i][c];
+    if (yi < nrows) {
+      const float* v = &ds[warp][yi][yc];
       const float4 v0 = *reinterpret_cast<const float4*>(v), v1 = *reinterpret_cast<const float4*>(v + 4);
       uint4 o;
-      o.x = pack_bf16x2(bf16lo_to_f32(y.x) + v0.x, bf16hi_to_f32(y.x) + v0.y);
-      o.y = pack_bf16x2(bf16lo_to_f32(y.y) + v0.z, bf16hi_to_f32(y.y) + v0.w);
-      o.z = pack_bf16x2(bf16lo_to_f32(y.z) + v1.x, bf16hi_to_f32(y.z) + v1.y);
-      o.w = pack_bf16x2(bf16lo_to_f32(y.w) + v1.z, bf16hi_to_f32(y.w) + v1.w);
-      *reinterpret_cast<uint4*>(p.Y + row * p.ldy + n0 + c) = o;
+      o.x = pack_bf16x2(bf16lo_to_f32(yv.x) + v0.x, bf16hi_to_f32(yv.x) + v0.y);
+      o.y = pack_bf16x2(bf16lo_to_f32(yv.y) + v0.z, bf16hi_to_f32(yv.y) + v0.w);
+      o.z = pack_bf16x2(bf16lo_to_f32(yv.z) + v1.x, bf16hi_to_f32(yv.z) + v1.y);
+      o.w = pack_bf16x2(bf16lo_to_f32(yv.w) + v1.z, bf16hi_to_f32(yv.w) + v1.w);
+      *reinterpret_cast<uint4*>(p.Y + yrow * p.ldy + n0 + yc) = o;
     }
     __syncwarp();
   }

@@ -30,15 +30,14 @@ namespace k13 {
 
 constexpr int kRows = kLoraTileRows;
 constexpr int kChunk = 64;
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kMaxStages = 6;
 constexpr int kXBytes = kRows * kChunk * 2;
 constexpr int kTmemCols = 128;
 constexpr int kSmemMax = 74 * 1024;                 // three CTAs per SM
 
 struct Params {
-  const int32_t* tiles;                             // {first row, rows, request, 0}
-  const int32_t* requests;                          // [requests][2 slots]: ids, weights
+  const int32_t* tiles;                             // the plan's tile records
   __nv_bfloat16* U;                                 // [tiles][128][2 slots rank]
   int K, rank, slots, adapters, ks, stages;
 };
@@ -54,7 +53,7 @@ __host__ __device__ constexpr int body_bytes(int jr, int stages) {      // the r
   const int ring = stages * stage_bytes(jr), part = kRows * (jr + 4) * 4;
   return ring > part ? ring : part;
 }
-constexpr int smem_bytes(int jr, int stages) { return 1024 + (body_bytes(jr, stages) + 15) / 16 * 16 + 8 * (2 * kMaxStages + 2) + 16; }
+constexpr int smem_bytes(int jr, int stages) { return 1024 + (body_bytes(jr, stages) + 15) / 16 * 16 + 8 * (2 * kMaxStages + 2) + 16 + 4 * kLoraMaxTileWords; }
 
 __global__ void __launch_bounds__(kThreads)
 lora_tile_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmX128,
@@ -73,8 +72,10 @@ lora_tile_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_cons
   const uint32_t drain = acc_full + 8u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + off_bar + 8 * (2 * kMaxStages + 2));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int32_t* rec = reinterpret_cast<int32_t*>(tmem_slot + 4);   // the tile's record
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int32_t* rec_g = p.tiles + static_cast<size_t>(blockIdx.x) * lora_tile_words(p.slots);
   const int nck_all = p.K / kChunk;
   const int c0 = static_cast<int>(static_cast<long long>(nck_all) * blockIdx.y / p.ks);
   const int nck = static_cast<int>(static_cast<long long>(nck_all) * (blockIdx.y + 1) / p.ks) - c0;   // >= 1: ks <= K / 64
@@ -90,39 +91,35 @@ lora_tile_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_cons
     prefetch_tmap(&tmA);
   }
   if (warp == 1) tmem_alloc<kTmemCols>(smem_addr(tmem_slot));
+  if (warp == 2 && lane == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(rec_g));   // a hint: L2 is coherent
   grid_dependency_wait();                           // X (or the plan, or an adapter) may come from the previous kernel
   grid_launch_dependents();                         // kernel 14 counts on this coming after the wait
+  if (warp == 2 && lane < 4 + 2 * p.slots) rec[lane] = __ldcg(rec_g + lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int4 tile = *reinterpret_cast<const int4*>(p.tiles + static_cast<size_t>(blockIdx.x) * 4);
-  const int32_t* req = p.requests + static_cast<size_t>(tile.z) * 2 * p.slots;
+  const int row0 = rec[0], nrows = rec[1];
+  const int32_t* ids = rec + 4;
+  const float* weights = reinterpret_cast<const float*>(rec + 4 + p.slots);
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
-    const int slabs = (tile.y + 31) / 32;
-    int a_row = 0;                                  // lane j: first row of slot j's adapter in A; an empty slot's
-    if (lane < p.slots) {                           // rows lie past the pool and are read as zeros
-      const int id = req[lane];
-      a_row = (id < 0 ? p.adapters : id) * p.rank;
-    }
+    const int slabs = (nrows + 31) / 32;
     for (int c = 0; c < nck; ++c) {
       const int s = c % S;
       const uint32_t sb = base + s * stage_bytes(jr);
       if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty(s), ((c / S) & 1u) ^ 1u, abort_flag, 71))) break;
       if (elect_one()) {
         mbar_arrive_expect_tx(full(s), slabs * 4096 + jr * kChunk * 2);
-        if (slabs == 4) tma_load_2d(sb, &tmX128, (c0 + c) * kChunk, tile.x, full(s));
+        if (slabs == 4) tma_load_2d(sb, &tmX128, (c0 + c) * kChunk, row0, full(s));
         else
-          for (int i = 0; i < slabs; ++i) tma_load_2d(sb + i * 4096, &tmX, (c0 + c) * kChunk, tile.x + 32 * i, full(s));
+          for (int i = 0; i < slabs; ++i) tma_load_2d(sb + i * 4096, &tmX, (c0 + c) * kChunk, row0 + 32 * i, full(s));
+        for (int j = 0; j < p.slots; ++j)           // an empty slot's rows lie past the pool: read as zeros
+          tma_load_2d(sb + kXBytes + j * p.rank * kChunk * 2, &tmA, (c0 + c) * kChunk,
+                      (ids[j] < 0 ? p.adapters : ids[j]) * p.rank, full(s));
       }
       __syncwarp();
-      for (int j = 0; j < p.slots; ++j) {
-        const int row = __shfl_sync(0xFFFFFFFFu, a_row, j);
-        if (elect_one()) tma_load_2d(sb + kXBytes + j * p.rank * kChunk * 2, &tmA, (c0 + c) * kChunk, row, full(s));
-        __syncwarp();
-      }
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issue (one elected lane)
@@ -152,12 +149,12 @@ lora_tile_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_cons
   const int stride = jr + 4;                        // floats per row: 16-byte stores of 8 rows fall on all banks
   float* part = reinterpret_cast<float*>(gbase);
   {
-    const int row = warp * 32 + lane;
+    const int q = warp & 3, row = q * 32 + lane;    // two warps per lane quarter, taking 32 columns in turn
     const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(acc_full, 0, abort_flag, 73));
     tc_fence_after();
-    for (int c = 0; ok && c < jr; c += 32) {
+    for (int c = 32 * (warp / 4); ok && c < jr; c += 64) {
       uint32_t v[32];
-      tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+      tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, v);
       tmem_wait_ld_regs(v);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -172,9 +169,9 @@ lora_tile_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_cons
   cluster_sync_all();                               // every slice's partial is in its CTA's shared memory
   const int rpc = kRows / p.ks;
   const int pieces = jr / 4;
-  for (int i = threadIdx.x; i < rpc * pieces; i += kThreads) {
-    const int r = static_cast<int>(cluster_ctarank()) * rpc + i / pieces, c = i % pieces * 4;
-    if (r >= tile.y) continue;
+  const int first = static_cast<int>(cluster_ctarank()) * rpc;
+  for (int i = threadIdx.x; i < min(rpc, nrows - first) * pieces; i += kThreads) {
+    const int r = first + i / pieces, c = i % pieces * 4;
     float4 v[8];
 #pragma unroll
     for (int z = 0; z < 8; ++z)
@@ -184,8 +181,8 @@ lora_tile_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_cons
     for (int z = 1; z < 8; ++z)                     // in slice order
       if (z < p.ks) { u.x += v[z].x; u.y += v[z].y; u.z += v[z].z; u.w += v[z].w; }
     const int slot = c / p.rank;
-    const bool has = req[slot] >= 0;                // an empty slot adds nothing, whatever is in X
-    const float w = __int_as_float(req[p.slots + slot]);
+    const bool has = ids[slot] >= 0;                // an empty slot adds nothing, whatever is in X
+    const float w = weights[slot];
     const float uu[4] = {has ? u.x * w : 0.f, has ? u.y * w : 0.f, has ? u.z * w : 0.f, has ? u.w * w : 0.f};
     uint32_t h[4];
     float lo[4];
@@ -195,6 +192,7 @@ lora_tile_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_cons
     *reinterpret_cast<uint2*>(dst) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
     *reinterpret_cast<uint2*>(dst + jr) = make_uint2(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]));
   }
+  __syncwarp();
   if (*abort_flag) {
     // a wait ran out: let the MMAs and copies already issued finish before the memory goes away
     if (warp == 1) {
@@ -208,7 +206,8 @@ lora_tile_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_cons
     }
   }
   __syncwarp();
-  cluster_sync_all();                               // the peers have read this CTA's partial
+  cluster_arrive_relaxed();                         // the peers have read this CTA's partial; relaxed: nothing to
+  cluster_wait_acquire();                           // publish, and U's stores are not waited for
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc<kTmemCols>(tmem);
@@ -230,8 +229,7 @@ constexpr int kTmemCols = 512;
 static_assert(kTmemU + 2 * kLoraMaxRank <= kTmemCols, "tensor memory");
 
 struct Params {
-  const int32_t* tiles;
-  const int32_t* requests;
+  const int32_t* tiles;                             // the plan's tile records
   const __nv_bfloat16* U;                           // kernel 13's
   __nv_bfloat16* Y;
   long long ldy;
@@ -310,7 +308,8 @@ lora_tile_up_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  auto tile_of = [&](int t) { return __ldcg(reinterpret_cast<const int4*>(p.tiles) + t); };
+  const int tile_words = lora_tile_words(p.slots);
+  auto tile_of = [&](int t) { return __ldcg(reinterpret_cast<const int4*>(p.tiles + static_cast<size_t>(t) * tile_words)); };
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
@@ -326,7 +325,7 @@ lora_tile_up_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
       if (t != last) {                              // the plan is read once per tile, not per piece
         tile = tile_of(t);
         if (busy && lane < p.slots) {
-          const int id = __ldcg(p.requests + static_cast<size_t>(tile.z) * 2 * p.slots + lane);
+          const int id = __ldcg(p.tiles + static_cast<size_t>(t) * tile_words + 4 + lane);
           b_row = id < 0 ? -1 : id * p.N;
         }
         last = t;

@@ -29,7 +29,7 @@ class SvdqError(RuntimeError):
 class LoraPlanStruct(ctypes.Structure):
     """svdq_lora_plan of the header: the sizes of a packed plan."""
     _fields_ = [(n, ctypes.c_int32) for n in ("M", "requests", "slots", "adapters", "tiles", "copy_tiles", "groups",
-                                              "reserved")] + [("bytes", ctypes.c_int64)]
+                                              "copy_groups")] + [("bytes", ctypes.c_int64)]
 
 
 def _load():

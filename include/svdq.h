@@ -362,7 +362,7 @@ int awq_w4a16_linear(const void* X, const void* qweight, const void* scales,
  * Errors and asynchrony as svdq_w4a4_nvfp4_linear. */
 typedef struct {
   int32_t M, requests, slots, adapters;
-  int32_t tiles, copy_tiles, groups, reserved;
+  int32_t tiles, copy_tiles, groups, copy_groups;
   int64_t bytes;
 } svdq_lora_plan;
 

@@ -18,15 +18,13 @@ def _decode(plan):
     w = plan.words.view(torch.int32).numpy()
     s = plan.struct
     assert bytes(w[:2].tobytes()) == b"SVDQLORA"
-    assert list(w[2:9]) == [s.M, s.requests, s.slots, s.adapters, s.tiles, s.copy_tiles, s.groups]
-    at = 16 + (s.requests * 2 * s.slots + 3) // 4 * 4
-    req = w[16:16 + s.requests * 2 * s.slots].reshape(s.requests, 2, s.slots)
-    tiles = w[at:at + 4 * (s.tiles + s.copy_tiles)].reshape(-1, 4)
-    at += 4 * (s.tiles + s.copy_tiles)
-    gw = 28 + 16 * s.slots
-    groups = w[at:at + gw * s.groups].reshape(-1, gw)
-    assert (at + gw * s.groups) * 4 == s.bytes == plan.words.numel()
-    return req, tiles[:s.tiles], tiles[s.tiles:], groups
+    assert list(w[2:10]) == [s.M, s.requests, s.slots, s.adapters, s.tiles, s.copy_tiles, s.groups, s.copy_groups]
+    tw, gw = (4 + 2 * s.slots + 3) // 4 * 4, 28 + 16 * s.slots
+    nt, ng = s.tiles + s.copy_tiles, s.groups + s.copy_groups
+    tiles = w[16:16 + tw * nt].reshape(-1, tw)
+    groups = w[16 + tw * nt:16 + tw * nt + gw * ng].reshape(-1, gw)
+    assert (16 + tw * nt + gw * ng) * 4 == s.bytes == plan.words.numel()
+    return tiles[:s.tiles], tiles[s.tiles:], groups[:s.groups], groups[s.groups:]
 
 
 @pytest.mark.parametrize("seed", range(8))
@@ -40,18 +38,21 @@ def test_a_plan_covers_every_row_once(seed, slots):
     ids = r.integers(-1, 3, size=(n, slots))
     w = r.standard_normal((n, slots)).astype(np.float32)
     plan = P.LoraPlan(off, ids, w, M, 3, device="cpu")
-    req, tiles, copies, groups = _decode(plan)
-    assert np.array_equal(req[:, 0], ids) and np.array_equal(req[:, 1].view(np.float32), w)
+    tiles, copies, groups, copy_groups = _decode(plan)
     owner = np.full(M, -1)
     for s in range(n):
         owner[off[s]:off[s + 1]] = s
     seen = np.zeros(M, int)
-    for row, rows, s, _ in tiles:
+    for t in tiles:
+        row, rows, s = t[:3]
         assert 1 <= rows <= 128 and (owner[row:row + rows] == s).all() and (ids[s] >= 0).any()
+        assert np.array_equal(t[4:4 + slots], ids[s]) and np.array_equal(t[4 + slots:4 + 2 * slots].view(np.float32), w[s])
         seen[row:row + rows] += 1
-    for row, rows, s, _ in copies:
-        assert 1 <= rows <= 128 and s == -1
-        assert all(owner[m] < 0 or (ids[owner[m]] < 0).all() for m in range(row, row + rows))
+    untouched = [m for m in range(M) if owner[m] < 0 or (ids[owner[m]] < 0).all()]
+    for t in copies:
+        row, rows, s = t[:3]
+        assert 1 <= rows <= 128 and s == -1 and (t[4:4 + slots] == -1).all()
+        assert set(range(row, row + rows)) <= set(untouched)
         seen[row:row + rows] += 1
     for g in groups:
         assert 1 <= g[0] <= 16
@@ -60,13 +61,17 @@ def test_a_plan_covers_every_row_once(seed, slots):
             assert np.array_equal(g[4:4 + slots], ids[s]) and (ids[s] >= 0).any()
             assert np.array_equal(g[28 + i * slots:28 + (i + 1) * slots].view(np.float32), w[s])
             seen[g[12 + i]] += 1
+    for g in copy_groups:
+        assert 1 <= g[0] <= 16 and (g[4:12] == -1).all()
+        assert set(g[12:12 + g[0]]) <= set(untouched)
+        seen[g[12:12 + g[0]]] += 1
     assert (seen == 1).all()
 
 
 def test_rows_of_requests_with_the_same_adapters_share_groups():
     plan = P.LoraPlan(list(range(65)), np.arange(64) % 4, np.ones(64), 64, 4, device="cpu")
     assert plan.struct.groups == 4 and plan.struct.tiles == 0
-    groups = _decode(plan)[3]
+    groups = _decode(plan)[2]
     assert [list(g[12:28]) for g in groups] == [list(range(a, 64, 4)) for a in range(4)]
 
 
