@@ -897,13 +897,21 @@ static bool lora_plan_ok(const svdq_lora_plan* p) {
                                                                 static_cast<size_t>(p->groups) + p->copy_groups).words);
 }
 
-// The workspace: kernel 13's U, then kernel 11's parts.
+// Slices of K in kernel 13: as many as keep the grid within one CTA per SM (its ring then takes all of the
+// shared memory), at least one, at most the 64-column chunks of K and four (kernel 14 reads every part).
+// 4608 x 2560 -> 7680, 64 ranks, both kernels: 45.6, 39.3, 38.2, 38.8, 42.4, 44.2 us with 1, 2, 3, 4, 6, 8
+// slices; 9001 x 10240 -> 2560, 128 ranks: 92, 69, 82, 77 us with 1, 2, 3, 4 (two is one CTA per SM).
+static int lora_tile_splits(int tiles, int K, int dev) {
+  return std::max(1, std::min({sm_count(dev) / std::max(1, tiles), K / 64, 4}));
+}
+
+// The workspace: kernel 13's parts, then kernel 11's.
 struct LoraWorkspace {
   size_t part, total;
 };
 static LoraWorkspace lora_workspace(const svdq_lora_plan* p, int K, int jr, int dev) {
   LoraWorkspace w;
-  w.part = static_cast<size_t>(p->tiles) * svdq::kLoraTileRows * 2 * jr * sizeof(uint16_t);
+  w.part = static_cast<size_t>(p->tiles) * lora_tile_splits(p->tiles, K, dev) * svdq::kLoraTileRows * jr * sizeof(float);
   w.total = w.part;
   if (p->groups > 0)
     w.total += static_cast<size_t>(p->groups) * lora_short_splits(p->groups, K, jr, dev) * svdq::kLoraGroupRows * jr *
@@ -945,30 +953,30 @@ static int lora_tiles_launch(const LoraCall& c, bool copy) {
   if (tiles > 0) {
     k13::Params p;
     p.tiles = c.tiles;
-    p.U = static_cast<__nv_bfloat16*>(c.ws);
+    p.parts = static_cast<float*>(c.ws);
     p.K = c.K;
     p.rank = c.rank;
     p.slots = c.plan->slots;
     p.adapters = c.plan->adapters;
-    p.stages = std::min(k13::kMaxStages, std::max(2, (k13::kSmemMax - 2048) / k13::stage_bytes(jr)));
-    // CTAs that share a tile's K: the most (1, 2, 4, 8) that keep the grid within one wave at three CTAs per
-    // SM; a cluster's CTAs share a GPC, whose odd SMs leave room for fewer of the larger ones
-    p.ks = 1;
-    while (p.ks < 8 && 2 * p.ks <= c.K / 64 && static_cast<int64_t>(tiles) * 2 * p.ks <= 3 * sms * 7 / 8) p.ks *= 2;
-    const int smem = k13::smem_bytes(jr, p.stages);
+    p.ks = lora_tile_splits(tiles, c.K, c.dev);
+    // one CTA per SM takes all of the shared memory, a larger grid leaves room for three
+    const int room = static_cast<int64_t>(tiles) * p.ks <= sms ? 227 * 1024 : 75 * 1024;
+    p.stages = std::min(k13::kMaxStages, (room - k13::kSmemExtra) / k13::stage_bytes(jr));
+    const int smem = p.stages * k13::stage_bytes(jr) + k13::kSmemExtra;
     CUtensorMap tX, tX128, tA;
     if (!make_tmap(&tX, c.X, bf, 2, c.M, c.K, k13::kChunk, 32, CU_TENSOR_MAP_SWIZZLE_128B, c.ldx) ||
         !make_tmap(&tX128, c.X, bf, 2, c.M, c.K, k13::kChunk, 128, CU_TENSOR_MAP_SWIZZLE_128B, c.ldx) ||
         !make_tmap(&tA, c.A, bf, 2, static_cast<uint64_t>(p.adapters) * c.rank, c.K, k13::kChunk, c.rank,
                    CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !set_smem_once<k13::lora_tile_down_kernel>(k13::kSmemMax, c.dev))
+        !set_smem_once<k13::lora_tile_down_kernel>(227 * 1024, c.dev))
       return SVDQ_ERR_CUDA;
-    if (!launch_pdl(k13::lora_tile_down_kernel, dim3(tiles, p.ks), k13::kThreads, smem, p.ks, c.stream, tX, tX128, tA, p))
+    if (!launch_pdl(k13::lora_tile_down_kernel, dim3(tiles, p.ks), k13::kThreads, smem, 1, c.stream, tX, tX128, tA, p))
       return SVDQ_ERR_CUDA;
   }
   k14::Params p;
   p.tiles = c.tiles;
-  p.U = static_cast<const __nv_bfloat16*>(c.ws);
+  p.parts = static_cast<const float*>(c.ws);
+  p.ks = lora_tile_splits(tiles, c.K, c.dev);
   p.Y = static_cast<__nv_bfloat16*>(c.Y);
   p.ldy = c.ldy;
   p.ntiles = tiles;

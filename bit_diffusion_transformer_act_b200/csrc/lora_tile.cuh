@@ -1,22 +1,26 @@
 // Kernels 13 and 14: the adapters of long requests, in tiles of up to 128 rows of one request.
 //
-// Mathematics.  out[m] = y[m] + sum_j B_j (w_j A_j x[m]).  Kernel 13 forms the tile's U = X [A_0; A_1; ...]^T
-// (128 x slots rank, fp32), scales column block j by the request's w_j and stores it as a high and a
-// low bf16 part side by side (U = hi + lo to 2^-16 relative).  Kernel 14 forms [hi | lo] [B_0 B_1 ... | B_0
-// B_1 ...]^T for a 128 x BN piece of the output, adds y and rounds once.
+// Mathematics.  out[m] = y[m] + sum_j B_j (w_j A_j x[m]).  Kernel 13 forms the tile's X [A_0; A_1; ...]^T (128 x
+// slots rank, fp32), each CTA over a slice of K, and writes its part.  Kernel 14 adds a tile's parts in
+// slice order, scales column block j by the request's w_j, splits the sum into a high and a low bf16 part
+// (U = hi + lo to 2^-16 relative), forms [hi | lo] [B_0 B_1 ... | B_0 B_1 ...]^T for a 128 x 128 piece of the
+// output, adds y and rounds once.
 //
 // What bounds them: memory.  With slots rank = 64 a row of X costs 2 K bytes and 2 K 64 flops, 64 flops per
 // byte, and a value of Y 4 bytes and 256 flops -- against 265 flops per byte of the card.  So the MMAs only
 // have to stay out of the way, and both kernels are streams: X through kernel 13, Y through kernel 14, each
 // once; A, B and U come from L2.
 //
-// Kernel 13: the CTAs of a cluster share a tile's K and sum their U over distributed shared memory in
-// slice order (no atomics, no scratch).  Kernel 14 is persistent: a CTA owns a run of (tile, BN columns)
-// pieces with the columns running first, so U is loaded once per tile; y and B arrive by TMA in a ring of
-// stages, the sum overwrites y in its stage, and the stage is stored from there.  U is the left operand and
-// lives in tensor memory (two tiles of it), which leaves shared memory to the ring.  32-row slabs that the
-// tile fills go out by TMA, a last partial slab row by row.  Rows of other requests in a partial tile are never
-// stored; each row of an MMA's result depends on its own row of the left operand only.
+// Kernel 13: grid of (tiles, slices of K).  The parts are small (512 slots rank bytes per row) and stay in L2; their
+// layout [4 ranks][128 rows] makes a warp's stores and kernel 14's loads whole lines.  Summing them over
+// distributed shared memory instead, in clusters along K, cost 4 to 5 us at the end of a 11 us kernel (4608 x 2560,
+// 64 ranks): the clusters start late, wait for their slowest CTA, and their remote loads are slow.
+// Kernel 14 is persistent: a CTA owns a run of (tile, 128 columns) pieces with the columns running first, so U
+// is formed once per tile; it is the left operand and lives in tensor memory (two tiles of it), which leaves
+// shared memory to the ring.  y and B arrive by TMA in a ring of stages, the sum overwrites y in its stage,
+// and the stage is stored from there: 32-row slabs that the tile fills by TMA, a last partial slab row by
+// row.  Rows of other requests in a partial tile are never stored; each row of an MMA's result depends on
+// its own row of the left operand only.
 //
 // Every mbarrier wait is bounded (see ptx.cuh).
 #pragma once
@@ -30,15 +34,14 @@ namespace k13 {
 
 constexpr int kRows = kLoraTileRows;
 constexpr int kChunk = 64;
-constexpr int kThreads = 256;
+constexpr int kThreads = 192;                       // producer, MMA, four read-out warps
 constexpr int kMaxStages = 6;
 constexpr int kXBytes = kRows * kChunk * 2;
 constexpr int kTmemCols = 128;
-constexpr int kSmemMax = 74 * 1024;                 // three CTAs per SM
 
 struct Params {
   const int32_t* tiles;                             // the plan's tile records
-  __nv_bfloat16* U;                                 // [tiles][128][2 slots rank]
+  float* parts;                                     // [tiles][ks][slots rank / 4][128 rows][4]
   int K, rank, slots, adapters, ks, stages;
 };
 
@@ -49,11 +52,7 @@ __device__ __forceinline__ uint32_t idesc_bf16(int n) {
 }
 
 __host__ __device__ constexpr int stage_bytes(int jr) { return kXBytes + jr * kChunk * 2; }
-__host__ __device__ constexpr int body_bytes(int jr, int stages) {      // the ring, later the partial U
-  const int ring = stages * stage_bytes(jr), part = kRows * (jr + 4) * 4;
-  return ring > part ? ring : part;
-}
-constexpr int smem_bytes(int jr, int stages) { return 1024 + (body_bytes(jr, stages) + 15) / 16 * 16 + 8 * (2 * kMaxStages + 2) + 16 + 4 * kLoraMaxTileWords; }
+constexpr int kSmemExtra = 1024 + 8 * (2 * kMaxStages + 2) + 16 + 4 * kLoraMaxTileWords;
 
 __global__ void __launch_bounds__(kThreads)
 lora_tile_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmX128,
@@ -64,7 +63,7 @@ lora_tile_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_cons
   uint8_t* gbase = smem_raw + (base - raw);
   const int jr = p.slots * p.rank;
   const int S = p.stages;
-  const uint32_t off_bar = static_cast<uint32_t>((body_bytes(jr, S) + 15) / 16 * 16);
+  const uint32_t off_bar = static_cast<uint32_t>(S * stage_bytes(jr));
   const uint32_t bars = base + off_bar;
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (kMaxStages + s); };
@@ -94,14 +93,13 @@ lora_tile_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_cons
   if (warp == 2 && lane == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(rec_g));   // a hint: L2 is coherent
   grid_dependency_wait();                           // X (or the plan, or an adapter) may come from the previous kernel
   grid_launch_dependents();                         // kernel 14 counts on this coming after the wait
-  if (warp == 2 && lane < 4 + 2 * p.slots) rec[lane] = __ldcg(rec_g + lane);
+  if (warp == 2 && lane < 4 + p.slots) rec[lane] = __ldcg(rec_g + lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int row0 = rec[0], nrows = rec[1];
   const int32_t* ids = rec + 4;
-  const float* weights = reinterpret_cast<const float*>(rec + 4 + p.slots);
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
@@ -142,57 +140,27 @@ lora_tile_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_cons
       }
       __syncwarp();
     }
-  }
-
-  // ---------------------------------------------------------------- U, summed over the cluster
-  // The last commit covers every MMA, and with them every copy into the ring: its space is free.
-  const int stride = jr + 4;                        // floats per row: 16-byte stores of 8 rows fall on all banks
-  float* part = reinterpret_cast<float*>(gbase);
-  {
-    const int q = warp & 3, row = q * 32 + lane;    // two warps per lane quarter, taking 32 columns in turn
-    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(acc_full, 0, abort_flag, 73));
-    tc_fence_after();
-    for (int c = 32 * (warp / 4); ok && c < jr; c += 64) {
-      uint32_t v[32];
-      tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, v);
-      tmem_wait_ld_regs(v);
+  } else {
+    // ---------------------------------------------------------------- read-out: a row per thread
+    const int q = warp & 3;
+    if (__all_sync(0xFFFFFFFFu, mbar_wait_bounded(acc_full, 0, abort_flag, 73))) {
+      tc_fence_after();
+      float4* dst = reinterpret_cast<float4*>(p.parts) +
+                    (static_cast<size_t>(blockIdx.x) * p.ks + blockIdx.y) * (jr / 4) * kRows + q * 32 + lane;
+      for (int c = 0; c < jr; c += 32) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, v);
+        tmem_wait_ld_regs(v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c + 4 * j < jr)
-          *reinterpret_cast<float4*>(part + row * stride + c + 4 * j) =
-              make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]), __uint_as_float(v[4 * j + 2]),
-                          __uint_as_float(v[4 * j + 3]));
+        for (int j = 0; j < 8; ++j)
+          if (c + 4 * j < jr)
+            dst[(c / 4 + j) * kRows] = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                                   __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+      }
+      tc_fence_before();
     }
-    tc_fence_before();
   }
-  __syncwarp();
-  cluster_sync_all();                               // every slice's partial is in its CTA's shared memory
-  const int rpc = kRows / p.ks;
-  const int pieces = jr / 4;
-  const int first = static_cast<int>(cluster_ctarank()) * rpc;
-  for (int i = threadIdx.x; i < min(rpc, nrows - first) * pieces; i += kThreads) {
-    const int r = first + i / pieces, c = i % pieces * 4;
-    float4 v[8];
-#pragma unroll
-    for (int z = 0; z < 8; ++z)
-      if (z < p.ks) v[z] = ld_dsmem_f32x4(part + r * stride + c, static_cast<uint32_t>(z));
-    float4 u = v[0];
-#pragma unroll
-    for (int z = 1; z < 8; ++z)                     // in slice order
-      if (z < p.ks) { u.x += v[z].x; u.y += v[z].y; u.z += v[z].z; u.w += v[z].w; }
-    const int slot = c / p.rank;
-    const bool has = ids[slot] >= 0;                // an empty slot adds nothing, whatever is in X
-    const float w = weights[slot];
-    const float uu[4] = {has ? u.x * w : 0.f, has ? u.y * w : 0.f, has ? u.z * w : 0.f, has ? u.w * w : 0.f};
-    uint32_t h[4];
-    float lo[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = k11::split_hi_lo(uu[j], lo[j]);
-    __nv_bfloat16* dst = p.U + (static_cast<size_t>(blockIdx.x) * kRows + r) * (2 * jr) + c;
-    *reinterpret_cast<uint2*>(dst) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-    *reinterpret_cast<uint2*>(dst + jr) = make_uint2(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]));
-  }
-  __syncwarp();
+  __syncthreads();
   if (*abort_flag) {
     // a wait ran out: let the MMAs and copies already issued finish before the memory goes away
     if (warp == 1) {
@@ -204,10 +172,8 @@ lora_tile_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_cons
       const uint64_t t0 = global_timer_ns();
       while (global_timer_ns() - t0 < 2000000ull) { }
     }
+    __syncthreads();
   }
-  __syncwarp();
-  cluster_arrive_relaxed();                         // the peers have read this CTA's partial; relaxed: nothing to
-  cluster_wait_acquire();                           // publish, and U's stores are not waited for
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc<kTmemCols>(tmem);
@@ -221,7 +187,7 @@ namespace k14 {
 constexpr int kRows = kLoraTileRows;
 constexpr int kGroups = 2;                          // epilogue groups of four warps, taking pieces in turn
 constexpr int kUWarp0 = 2 + 4 * kGroups;
-constexpr int kThreads = (kUWarp0 + 4) * 32;        // producer, MMA, epilogue, U loaders
+constexpr int kThreads = (kUWarp0 + 8) * 32;        // producer, MMA, epilogue, U makers
 constexpr int kMaxStages = 6;
 constexpr int kBN = 128;                            // output columns per piece
 constexpr int kTmemU = kGroups * kBN;               // tensor memory: an accumulator per group, then two U
@@ -230,7 +196,8 @@ static_assert(kTmemU + 2 * kLoraMaxRank <= kTmemCols, "tensor memory");
 
 struct Params {
   const int32_t* tiles;                             // the plan's tile records
-  const __nv_bfloat16* U;                           // kernel 13's
+  const float* parts;                               // kernel 13's
+  int ks;
   __nv_bfloat16* Y;
   long long ldy;
   int ntiles;                                       // tiles with adapters; tiles after them are copied
@@ -292,7 +259,7 @@ lora_tile_up_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < S; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 5); }   // four epilogue warps, the MMAs
-    for (int u = 0; u < 2; ++u) { mbar_init(u_full(u), 4); mbar_init(u_empty(u), 1); }
+    for (int u = 0; u < 2; ++u) { mbar_init(u_full(u), 8); mbar_init(u_empty(u), 1); }
     for (int b = 0; b < kGroups; ++b) { mbar_init(acc_full(b), 1); mbar_init(acc_empty(b), 4); }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -394,27 +361,59 @@ lora_tile_up_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
       __syncwarp();
     }
   } else if (warp >= kUWarp0) {
-    // ---------------------------------------------------------------- U loaders: a row per thread
+    // ---------------------------------------------------------------- U: a row per thread, two warps per lane
+    // quarter taking blocks of 16 ranks in turn
     if (p.early) grid_dependency_wait();            // kernel 13 is done
     const int q = warp & 3;
     const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(kTmemU);
+    const size_t part = static_cast<size_t>(jr / 4) * kRows;   // float4 per part
     int nu = 0;
     for (int t = i0 / p.chunks; t < p.ntiles && t * static_cast<long long>(p.chunks) < i1; ++t, ++nu) {
-      const uint4* src = reinterpret_cast<const uint4*>(p.U + (static_cast<size_t>(t) * kRows + q * 32 + lane) * (2 * jr));
+      const int32_t* rec = p.tiles + static_cast<size_t>(t) * tile_words + 4;
+      const float4* src = reinterpret_cast<const float4*>(p.parts) + t * p.ks * part + q * 32 + lane;
       if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(u_empty(nu & 1), ((nu >> 1) & 1u) ^ 1u, abort_flag, 82))) break;
       tc_fence_after();
-#pragma unroll 2
-      for (int c = 0; c < jr; c += 16) {            // 16 words = 32 values
-        uint32_t v[16];
+      const uint32_t tu = trow + static_cast<uint32_t>((nu & 1) * kLoraMaxRank);
+      for (int c = (warp - kUWarp0) / 4 * 16; c < jr; c += 32) {
+        float4 u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int z = 0; z < p.ks; z += 4) {         // 16 loads in flight; added in slice order
+          float4 v[4][4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (z + k < p.ks) v[k][j] = __ldcg(src + (z + k) * part + (c / 4 + j) * kRows);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (z + k < p.ks) {
+                u[j].x += v[k][j].x;
+                u[j].y += v[k][j].y;
+                u[j].z += v[k][j].z;
+                u[j].w += v[k][j].w;
+              }
+        }
+        const int slot = c / p.rank;
+        const bool has = __ldcg(rec + slot) >= 0;   // an empty slot adds nothing, whatever is in X
+        const float w = __int_as_float(__ldcg(rec + p.slots + slot));
+        uint32_t hi[8], lo[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint4 w = __ldcg(src + c / 4 + j);
-          v[4 * j] = w.x;
-          v[4 * j + 1] = w.y;
-          v[4 * j + 2] = w.z;
-          v[4 * j + 3] = w.w;
+          const float uu[4] = {has ? u[j].x * w : 0.f, has ? u[j].y * w : 0.f, has ? u[j].z * w : 0.f,
+                               has ? u[j].w * w : 0.f};
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float l0, l1;
+            const uint32_t h0 = k11::split_hi_lo(uu[2 * k], l0), h1 = k11::split_hi_lo(uu[2 * k + 1], l1);
+            hi[2 * j + k] = h0 | (h1 << 16);
+            lo[2 * j + k] = pack_bf16x2(l0, l1);
+          }
         }
-        tmem_st_32x32b_x16(trow + static_cast<uint32_t>((nu & 1) * kLoraMaxRank + c), v);
+        tmem_st_32x32b_x8(tu + static_cast<uint32_t>(c / 2), hi);
+        tmem_st_32x32b_x8(tu + static_cast<uint32_t>((jr + c) / 2), lo);
       }
       tmem_wait_st();
       tc_fence_before();
