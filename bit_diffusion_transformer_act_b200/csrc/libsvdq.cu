@@ -1219,7 +1219,7 @@ int svdq_qk_norm_rope(const void* Q, int64_t q_row_stride, int64_t q_head_stride
   p.P = P;
   p.M = M;
   p.q_heads = q_heads;
-  p.heads = q_heads + k_heads;
+  p.k_heads = k_heads;
   p.D = D;
   p.eps = eps;
   // 8 pairs per lane where runs of 8 fit the head and the rotated columns, else 4
@@ -1227,12 +1227,12 @@ int svdq_qk_norm_rope(const void* Q, int64_t q_row_stride, int64_t q_head_stride
   int lpr = 1;
   while (lpr * 2 * V < D) lpr *= 2;
   // warps per token: as many as the token's heads can use while the grid has fewer than 16 per SM
-  const int passes = (p.heads + 32 / lpr - 1) / (32 / lpr);
+  const int passes = (std::max(q_heads, k_heads) + 32 / lpr - 1) / (32 / lpr);
   const int64_t most = 16ll * sm_count(dev);
   p.parts = 1;
   while (p.parts < 8 && 2 * p.parts <= passes && M * 2ll * p.parts <= most) p.parts *= 2;
   const int64_t blocks = (static_cast<int64_t>(M) * p.parts + k9::kThreads / 32 - 1) / (k9::kThreads / 32);
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(blocks, 4ll * sm_count(dev))));
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(k9::kBlocksPerSm) * sm_count(dev))));
 #define SVDQ_ROPE_CASE(V_, L_)                                                                                  \
   if (V == V_ && lpr == L_)                                                                                     \
     return launch_pdl(pairing ? k9::qk_norm_rope_kernel<V_, L_, true> : k9::qk_norm_rope_kernel<V_, L_, false>, \

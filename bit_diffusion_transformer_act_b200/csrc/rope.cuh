@@ -23,6 +23,7 @@ namespace k9 {
 constexpr int kMaxAxes = 8;
 constexpr int kMaxPairs = 128;             // head_dim <= 256
 constexpr int kThreads = 256;
+constexpr int kBlocksPerSm = 3;
 
 struct Freqs {
   double f[kMaxPairs];                     // turns per unit of position, in pair order
@@ -39,7 +40,7 @@ struct Params {
   const __nv_bfloat16 *wq, *wk;            // [D] or null (no normalisation)
   const void* pos;                         // [P, axes] int32, or float32
   int pos_float;
-  int axes, P, M, q_heads, heads;          // heads: of q and k together
+  int axes, P, M, q_heads, k_heads;
   int D, rot;                              // head width, rotated columns
   int parts;                               // warps that share a token's heads
   float eps;
@@ -71,113 +72,169 @@ __device__ __forceinline__ void store_v(__nv_bfloat16* p, const uint32_t (&r)[V 
   else *reinterpret_cast<uint2*>(p) = make_uint2(r[0], r[1]);
 }
 
-// A unit is V pairs, held by one lane as two runs of V elements; LPR lanes (a power of two, at
-// least D / 2V) hold a head's row, and a warp 32 / LPR heads of one token at a time.  A lane's
-// unit does not change, so its sines and cosines are formed once per token and used for all of
-// the token's heads.
+// A unit is V pairs, held by one lane as two runs of V elements; LPR lanes (a power of two, at least D / 2V)
+// hold a head's row, and a warp 32 / LPR heads of one token at a time.  A lane's unit does not change, so the
+// token's sines and cosines are formed once for all its heads -- each lane forms its share of the pairs of
+// its unit, the lanes that hold the unit for other heads the rest -- and the norm weights are folded into
+// them: with u = x / rms, pair (x0, x1) becomes (u0 w0 c - u1 w1 s, u0 w0 s + u1 w1 c), four factors per pair
+// and one scale per head.
+//
+// Bound by memory (q and k read and written once: 4 bytes a value) if the instructions are few: with the
+// sines formed by every lane, the weights unpacked per head and scalar arithmetic the kernel issued
+// 2940 warp instructions per token of 40 heads and took 61 us at 9216 tokens (floor 29 us).
 template <int V, int LPR, bool kHalf>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 qk_norm_rope_kernel(const __grid_constant__ Params p, const __grid_constant__ Freqs fr) {
   constexpr int HPW = 32 / LPR;
+  constexpr int kShare = HPW >= V ? 1 : V / HPW;   // pairs of its unit whose angle a lane forms
   const int lane = threadIdx.x % 32;
   const int u = lane % LPR, sub = lane / LPR;
   const bool active = u * 2 * V < p.D;             // lanes past the row's end hold nothing
   const bool turned = u * 2 * V < p.rot;           // units past the rotated columns are only normalised
   const int e0 = turned && kHalf ? V * u : 2 * V * u;
-  const int e1 = turned && kHalf ? p.rot / 2 + V * u : 2 * V * u + V;
-  double f[V];
-  int ax[V];
+  const int run = turned && kHalf ? p.rot / 2 : V;  // from the unit's first run to its second
+  double f[kShare];
+  int ax[kShare];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    f[j] = turned ? fr.f[V * u + j] : 0.0;
-    ax[j] = turned ? fr.axis[V * u + j] : 0;
+  for (int j = 0; j < kShare; ++j) {
+    const int i = V * u + sub * kShare + j;        // (lanes with sub >= V have nothing to form)
+    f[j] = turned && sub * kShare < V ? fr.f[i] : 0.0;
+    ax[j] = turned && sub * kShare < V ? fr.axis[i] : 0;
   }
   grid_dependency_wait();                          // q and k come from the previous kernel
   grid_launch_dependents();
-  uint32_t w0[2][V / 2], w1[2][V / 2];             // norm weights of q and k
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const __nv_bfloat16* w = t ? p.wk : p.wq;
-#pragma unroll
-    for (int j = 0; j < V / 2; ++j) w0[t][j] = w1[t][j] = 0u;
-    if (w && active) {
-      load_v<V>(w + e0, w0[t]);
-      load_v<V>(w + e1, w1[t]);
-    }
-  }
   const int warps = gridDim.x * (kThreads / 32);
   const int wid = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
   const int part = wid % p.parts;
   const float inv_d = 1.0f / static_cast<float>(p.D);
-  for (long long m = wid / p.parts; m < p.M; m += warps / p.parts) {
-    float c[V], s[V];
-    if (turned) {
-      const long long at = static_cast<long long>(static_cast<int>(m) % p.P) * p.axes;
+  const int step = p.parts * HPW;
+  const long long m_step = warps / p.parts;
+  for (long long m = wid / p.parts; m < p.M; m += m_step) {
+    float cs[kShare], sn[kShare];
+    const long long at = static_cast<long long>(static_cast<int>(m) % p.P) * p.axes;
 #pragma unroll
-      for (int j = 0; j < V; ++j) sincos_turns(position(p.pos, p.pos_float, at + ax[j]) * f[j], s[j], c[j]);
-    }
-    for (int h0 = part * HPW; h0 < p.heads; h0 += p.parts * HPW) {
-      const int h = h0 + sub;
-      const bool on = active && h < p.heads;
-      const bool is_k = h >= p.q_heads;
-      const View& vi = is_k ? p.k : p.q;
-      const View& vo = is_k ? p.ok : p.oq;
-      const int hh = is_k ? h - p.q_heads : h;
+    for (int j = 0; j < kShare; ++j) sincos_turns(position(p.pos, p.pos_float, at + ax[j]) * f[j], sn[j], cs[j]);
+    // This lane's heads of q or of k: written twice into the code, so that the strides and pointers stay
+    // operands from the parameters instead of selected values.
+    auto rotate = [&](const View& vi, const View& vo, const __nv_bfloat16* w, int heads) {
+      const int h0 = part * HPW;
+      if (h0 >= heads) return;
+      const __nv_bfloat16* src = vi.ptr + m * vi.row + (h0 + sub) * vi.head + e0;
+      __nv_bfloat16* dst = vo.ptr + m * vo.row + (h0 + sub) * vo.head + e0;
+      const long long src_step = step * vi.head, dst_step = step * vo.head;
+      int left = active ? heads - h0 - sub : 0;    // > 0: this lane holds a head
       uint32_t r0[V / 2], r1[V / 2];
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) r0[j] = r1[j] = 0u;
-      if (on) {
-        const __nv_bfloat16* src = vi.ptr + m * vi.row + hh * vi.head;
-        load_v<V>(src + e0, r0);
-        load_v<V>(src + e1, r1);
+      if (left > 0) {
+        load_v<V>(src, r0);
+        load_v<V>(src + run, r1);
       }
-      float x0[V], x1[V];                          // the unit's two runs
+      // the factors of pairs 2 i and 2 i + 1 side by side: y0 = x0 f00 + x1 f01, y1 = x0 f10 + x1 f11
+      uint64_t f00[V / 2], f01[V / 2], f10[V / 2], f11[V / 2];
+      {
+        uint32_t w0[V / 2], w1[V / 2];
 #pragma unroll
-      for (int j = 0; j < V / 2; ++j) {
-        x0[2 * j] = bf16lo_to_f32(r0[j]);
-        x0[2 * j + 1] = bf16hi_to_f32(r0[j]);
-        x1[2 * j] = bf16lo_to_f32(r1[j]);
-        x1[2 * j + 1] = bf16hi_to_f32(r1[j]);
-      }
-      float ss = 0.f;                              // no branch here: lanes of q and of k may share a warp
-#pragma unroll
-      for (int j = 0; j < V; ++j) ss = fmaf(x0[j], x0[j], fmaf(x1[j], x1[j], ss));
-#pragma unroll
-      for (int o = LPR / 2; o > 0; o /= 2) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-      if (is_k ? p.wk != nullptr : p.wq != nullptr) {
-        const float rstd = rsqrtf(fmaf(ss, inv_d, p.eps));
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) {
-          const uint32_t a = is_k ? w0[1][j] : w0[0][j], b = is_k ? w1[1][j] : w1[0][j];
-          x0[2 * j] *= rstd * bf16lo_to_f32(a);
-          x0[2 * j + 1] *= rstd * bf16hi_to_f32(a);
-          x1[2 * j] *= rstd * bf16lo_to_f32(b);
-          x1[2 * j + 1] *= rstd * bf16hi_to_f32(b);
+        for (int j = 0; j < V / 2; ++j) w0[j] = w1[j] = 0x3F803F80u;
+        if (w && active) {
+          load_v<V>(w + e0, w0);
+          load_v<V>(w + e0 + run, w1);
         }
-      }
-      if (turned) {
-        // pair j: halves (x0[j], x1[j]); interleaved (x[2j], x[2j + 1]) of the 2V contiguous elements
+        float g[4][V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          float& a = kHalf ? x0[j] : (j < V / 2 ? x0[2 * j] : x1[2 * j - V]);
-          float& b = kHalf ? x1[j] : (j < V / 2 ? x0[2 * j + 1] : x1[2 * j + 1 - V]);
-          const float y0 = a * c[j] - b * s[j];
-          const float y1 = a * s[j] + b * c[j];
-          a = y0;
-          b = y1;
+          const float c = __shfl_sync(0xFFFFFFFFu, cs[j % kShare], u + LPR * (j / kShare));
+          const float s = __shfl_sync(0xFFFFFFFFu, sn[j % kShare], u + LPR * (j / kShare));
+          // weights of the pair's two elements: of the two runs (halves), or neighbours
+          const uint32_t a = kHalf ? w0[j / 2] : (j < V / 2 ? w0[j % (V / 2)] : w1[j % (V / 2)]);
+          const uint32_t b = kHalf ? w1[j / 2] : a;
+          const float wa = kHalf && j % 2 ? bf16hi_to_f32(a) : bf16lo_to_f32(a);
+          const float wb = kHalf && j % 2 == 0 ? bf16lo_to_f32(b) : bf16hi_to_f32(b);
+          g[0][j] = turned ? wa * c : wa;
+          g[1][j] = -wb * s;
+          g[2][j] = wa * s;
+          g[3][j] = turned ? wb * c : wb;
         }
-      }
-      if (on) {
 #pragma unroll
-        for (int j = 0; j < V / 2; ++j) {
-          r0[j] = pack_bf16x2(x0[2 * j], x0[2 * j + 1]);
-          r1[j] = pack_bf16x2(x1[2 * j], x1[2 * j + 1]);
+        for (int i = 0; i < V / 2; ++i) {
+          f00[i] = f32x2_pack(g[0][2 * i], g[0][2 * i + 1]);
+          f01[i] = f32x2_pack(g[1][2 * i], g[1][2 * i + 1]);
+          f10[i] = f32x2_pack(g[2][2 * i], g[2][2 * i + 1]);
+          f11[i] = f32x2_pack(g[3][2 * i], g[3][2 * i + 1]);
         }
-        __nv_bfloat16* dst = vo.ptr + m * vo.row + hh * vo.head;
-        store_v<V>(dst + e0, r0);
-        store_v<V>(dst + e1, r1);
       }
-    }
+      // Units past the rotated columns add no cross terms: an infinity must not reach its neighbour.
+#pragma unroll 1
+      for (int n = heads - h0; n > 0; n -= step) {
+        uint64_t x0[V / 2], x1[V / 2];             // first and second elements of pairs 2 i, 2 i + 1
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+          const uint32_t a = kHalf ? r0[i] : (i < V / 4 ? r0[(2 * i) % (V / 2)] : r1[(2 * i) % (V / 2)]);
+          const uint32_t b = kHalf ? r1[i] : (i < V / 4 ? r0[(2 * i + 1) % (V / 2)] : r1[(2 * i + 1) % (V / 2)]);
+          // halves: a, b hold (x0 of both pairs), (x1 of both pairs); interleaved: pair 2 i, pair 2 i + 1
+          x0[i] = kHalf ? f32x2_pack(bf16lo_to_f32(a), bf16hi_to_f32(a)) : f32x2_pack(bf16lo_to_f32(a), bf16lo_to_f32(b));
+          x1[i] = kHalf ? f32x2_pack(bf16lo_to_f32(b), bf16hi_to_f32(b)) : f32x2_pack(bf16hi_to_f32(a), bf16hi_to_f32(b));
+        }
+        const bool store = left > 0;
+        left -= step;
+        src += src_step;
+        if (left > 0) {                            // the next heads, while these are worked on
+          load_v<V>(src, r0);
+          load_v<V>(src + run, r1);
+        }
+        float scale = 1.f;
+        if (w) {
+          uint64_t q0 = f32x2_mul(x0[0], x0[0]), q1 = f32x2_mul(x1[0], x1[0]);
+#pragma unroll
+          for (int i = 1; i < V / 2; ++i) {
+            q0 = f32x2_fma(x0[i], x0[i], q0);
+            q1 = f32x2_fma(x1[i], x1[i], q1);
+          }
+          float sa, sb, sc, sd;
+          f32x2_unpack(q0, sa, sb);
+          f32x2_unpack(q1, sc, sd);
+          float ss = (sa + sb) + (sc + sd);
+          if (LPR > 1 && !store) ss = 0.f;         // lanes past the row's end
+#pragma unroll
+          for (int o = LPR / 2; o > 0; o /= 2) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+          scale = rsqrtf(fmaf(ss, inv_d, p.eps));
+        }
+        const uint64_t scale2 = f32x2_pack(scale, scale);
+        uint32_t o0[V / 2], o1[V / 2];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+          uint64_t y0 = f32x2_mul(x0[i], f00[i]), y1 = f32x2_mul(x1[i], f11[i]);
+          if (turned) {
+            y0 = f32x2_fma(x1[i], f01[i], y0);
+            y1 = f32x2_fma(x0[i], f10[i], y1);
+          }
+          y0 = f32x2_mul(y0, scale2);
+          y1 = f32x2_mul(y1, scale2);
+          float a0, a1, b0, b1;                    // y0 and y1 of pair 2 i, of pair 2 i + 1
+          f32x2_unpack(y0, a0, b0);
+          f32x2_unpack(y1, a1, b1);
+          const uint32_t first = kHalf ? pack_bf16x2(a0, b0) : pack_bf16x2(a0, a1);
+          const uint32_t second = kHalf ? pack_bf16x2(a1, b1) : pack_bf16x2(b0, b1);
+          if (kHalf) {
+            o0[i] = first;
+            o1[i] = second;
+          } else if (i < V / 4) {
+            o0[(2 * i) % (V / 2)] = first;
+            o0[(2 * i + 1) % (V / 2)] = second;
+          } else {
+            o1[(2 * i) % (V / 2)] = first;
+            o1[(2 * i + 1) % (V / 2)] = second;
+          }
+        }
+        if (store) {
+          store_v<V>(dst, o0);
+          store_v<V>(dst + run, o1);
+        }
+        dst += dst_step;
+      }
+    };
+    rotate(p.q, p.oq, p.wq, p.q_heads);
+    rotate(p.k, p.ok, p.wk, p.k_heads);
   }
 }
 
