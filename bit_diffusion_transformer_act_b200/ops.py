@@ -127,6 +127,20 @@ def _require(t, dtype, shape, name):
     _on_device(t, name)
 
 
+def _device_of(t):
+    """The current device where `t` is a CUDA tensor, else -1 (the checks of the call's tensors refuse it)."""
+    return torch._C._cuda_getDevice() if isinstance(t, torch.Tensor) and t.is_cuda else -1
+
+
+def _addr(t, dtype, shape, name, dev):
+    """The address of a tensor of that type and shape, contiguous and on device `dev` (the current one).
+    One pass of cheap comparisons; what they reject, _require explains."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous() and
+            t.get_device() == dev >= 0):
+        _require(t, dtype, shape, name)
+    return t.data_ptr()
+
+
 def _l1_section_end(K, rank):
     """Bytes of the packed blob that the activation kernel reads: the 1 KB header and the
     low-rank down factor section that follows it (two bf16 [rank, K] parts, hi and lo).  The C
@@ -542,33 +556,50 @@ class LoraPlan:
         _check("svdq_lora_plan_pack",
                LIB.svdq_lora_plan_pack(_np_ptr(off), _np_ptr(ids), _np_ptr(w), self.requests, self.slots, self.rows,
                                        self.adapters, _np_ptr(host), nbytes, ctypes.byref(self.struct)))
-        self.words = torch.from_numpy(host[: self.struct.bytes]).to(device)
+        self._keep(torch.from_numpy(host[: self.struct.bytes]).to(device))
 
     @classmethod
     def from_parts(cls, words, sizes):
         """The plan of a packed blob on the device and its struct's fields (`sizes()`)."""
         self = cls.__new__(cls)
         self.struct = LoraPlanStruct(*sizes)
-        self.words = words
         self.rows, self.requests = self.struct.M, self.struct.requests
         self.slots, self.adapters = self.struct.slots, self.struct.adapters
+        _require_blob(words, "plan", self.struct.bytes)
+        self._keep(words)
         return self
+
+    def _keep(self, words):
+        self.words = words
+        self.nbytes = self.struct.bytes
+        self.struct_ref = ctypes.byref(self.struct)
+        self._workspace = {}
+
+    def workspace_bytes(self, K, rank, dev):
+        """svdq_lora_workspace_bytes on the current device `dev` (a number that follows from the sizes)."""
+        n = self._workspace.get((K, rank, dev))
+        if n is None:
+            n = self._workspace[(K, rank, dev)] = svdq_lora_workspace_bytes(self, K, rank)
+        return n
 
     def sizes(self):
         return [getattr(self.struct, n) for n, _ in LoraPlanStruct._fields_]
 
 
-def _row_strided(t, rows, cols, name):
-    """A bf16 [rows, cols] CUDA tensor whose rows may be apart (a column window of a wider one); its row
-    stride."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or tuple(t.shape) != (rows, cols):
+def _row_strided(t, rows, cols, name, dev):
+    """A bf16 [rows, cols] tensor on device `dev` (the current one) whose rows may be apart (a column window
+    of a wider one): (address, row stride)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.shape != (rows, cols):
         raise ValueError(f"{name}: expected a torch.bfloat16 tensor of shape {(rows, cols)}, got "
                          f"{getattr(t, 'dtype', type(t))} {tuple(getattr(t, 'shape', ()))}")
-    ld = t.stride(0) if rows > 1 else max(cols, t.stride(0))
-    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+    ld, inner = t.stride()
+    if rows <= 1:
+        ld = max(cols, ld)
+    if (cols > 1 and inner != 1) or ld < cols:
         raise ValueError(f"{name}: rows must be contiguous and must not overlap")
-    _on_device(t, name)
-    return ld
+    if not t.get_device() == dev >= 0:
+        _on_device(t, name)
+    return t.data_ptr(), ld
 
 
 def svdq_lora_workspace_bytes(plan, K, rank):
@@ -589,52 +620,64 @@ def svdq_lora_add(X, Y, A, B, plan, out=None, workspace=None):
     N = Y.shape[1]
     if M != plan.rows or adapters != plan.adapters:
         raise ValueError(f"the plan is for {plan.rows} rows and {plan.adapters} adapters, got {M} and {adapters}")
-    ldx = _row_strided(X, M, K, "X")
-    ldyin = _row_strided(Y, M, N, "Y")
-    _require(A, torch.bfloat16, (adapters, rank, K), "A")
-    _require(B, torch.bfloat16, (adapters, N, rank), "B")
-    _require_blob(plan.words, "plan", plan.struct.bytes)
+    bf16 = torch.bfloat16
+    dev = _device_of(X)
+    xp, ldx = _row_strided(X, M, K, "X", dev)
+    yp, ldyin = _row_strided(Y, M, N, "Y", dev)
+    ap = _addr(A, bf16, (adapters, rank, K), "A", dev)
+    bp = _addr(B, bf16, (adapters, N, rank), "B", dev)
+    words = plan.words
+    if words.get_device() != dev:
+        _require_blob(words, "plan", plan.struct.bytes)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=Y.device)
-    ldy = _row_strided(out, M, N, "out")
-    ws_bytes = svdq_lora_workspace_bytes(plan, K, rank)
+        out = Y.new_empty((M, N))
+        op, ldy = out.data_ptr(), N
+    else:
+        op, ldy = _row_strided(out, M, N, "out", dev)
+    ws_bytes = plan.workspace_bytes(K, rank, dev)
     if workspace is None:
-        workspace = torch.empty((ws_bytes,), dtype=torch.uint8, device=Y.device)
-    _require_blob(workspace, "workspace", ws_bytes)
-    st = LIB.svdq_lora_add(_ptr(X), ldx, _ptr(Y), ldyin, _ptr(A), _ptr(B), ctypes.byref(plan.struct), _ptr(plan.words),
-                           plan.words.numel(), M, N, K, rank, _ptr(workspace), workspace.numel(), _ptr(out), ldy,
-                           _stream())
-    _check("svdq_lora_add", st)
+        workspace = words.new_empty((ws_bytes,))
+    else:
+        _require_blob(workspace, "workspace", ws_bytes)
+    st = LIB.svdq_lora_add(xp, ldx, yp, ldyin, ap, bp, plan.struct_ref, words.data_ptr(), plan.nbytes, M, N, K, rank,
+                           workspace.data_ptr(), workspace.numel(), op, ldy, torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check("svdq_lora_add", st)
     return out
 
 
 def _rope_axes(positions, axes_dims, theta):
-    """Checked positions and the ctypes arrays of the axes: (P, axes, is_float, dims, thetas)."""
-    if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.float32) or \
+    """Checked positions and the ctypes arrays of the axes: (device, P, axes, is_float, dims, thetas)."""
+    is_float = isinstance(positions, torch.Tensor) and positions.dtype is torch.float32
+    if not isinstance(positions, torch.Tensor) or not (is_float or positions.dtype is torch.int32) or \
             positions.dim() != 2 or not positions.is_contiguous():
         raise ValueError("positions: expected a contiguous int32 or float32 tensor [P, axes]")
-    _on_device(positions, "positions")
+    dev = _device_of(positions)
+    if positions.get_device() != dev or dev < 0:
+        _on_device(positions, "positions")
     P, axes = positions.shape
-    thetas = [theta] * axes if isinstance(theta, (int, float)) else list(theta)
+    thetas = [theta] * axes if isinstance(theta, (int, float)) else theta
     if len(axes_dims) != axes or len(thetas) != axes:
         raise ValueError(f"{axes} axes need {axes} widths and one theta or {axes}")
-    return (P, axes, int(positions.dtype == torch.float32), (ctypes.c_int32 * axes)(*axes_dims),
-            (ctypes.c_double * axes)(*thetas))
+    return dev, P, axes, int(is_float), (ctypes.c_int32 * axes)(*axes_dims), (ctypes.c_double * axes)(*thetas)
 
 
 _PAIRINGS = {"interleaved": 0, "half": 1}
 
 
-def _heads(t, M, D, name):
-    """A bf16 [M, heads, D] CUDA tensor with any strides over tokens and heads."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != M or \
+def _heads(t, M, D, name, dev):
+    """A bf16 [M, heads, D] tensor on device `dev` (the current one) with any strides over tokens and heads:
+    (address, token stride, head stride, heads)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[0] != M or \
             t.shape[2] != D:
         raise ValueError(f"{name}: expected a torch.bfloat16 tensor [{M}, heads, {D}], got "
                          f"{getattr(t, 'dtype', type(t))} {tuple(getattr(t, 'shape', ()))}")
-    if t.stride(2) != 1:
+    row, head, inner = t.stride()
+    if inner != 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
-    _on_device(t, name)
-    return t.shape[1], t.stride(0), t.stride(1)
+    if not t.get_device() == dev >= 0:
+        _on_device(t, name)
+    return t.data_ptr(), row, head, t.shape[1]
 
 
 def svdq_qk_norm_rope(q, k, norm_wq, norm_wk, eps, positions, axes_dims, theta, pairing="interleaved", out_q=None,
@@ -646,50 +689,54 @@ def svdq_qk_norm_rope(q, k, norm_wq, norm_wk, eps, positions, axes_dims, theta, 
     pairing "interleaved" or "half".  out_q / out_k: q / k themselves for in place, tensors of their
     shape, or None for new ones.  Returns (out_q, out_k)."""
     M, _, D = (q if q is not None else k).shape
-    P, axes, is_float, dims, thetas = _rope_axes(positions, axes_dims, theta)
+    dev, P, axes, is_float, dims, thetas = _rope_axes(positions, axes_dims, theta)
     if pairing not in _PAIRINGS:
         raise ValueError(f"pairing: one of {sorted(_PAIRINGS)}, got {pairing!r}")
-    args = []
+    views = []
     outs = []
     for t, out, w, name in ((q, out_q, norm_wq, "q"), (k, out_k, norm_wk, "k")):
         if t is None:
             if out is not None or w is not None:
                 raise ValueError(f"out_{name} and norm_w{name} need {name}")
-            args.append((None, 0, 0, 0, None, 0, 0, None))
+            views.append((None, 0, 0, 0, None, 0, 0, None))
             outs.append(None)
             continue
-        heads, row, head = _heads(t, M, D, name)
+        tp, row, head, heads = _heads(t, M, D, name, dev)
         if out is None:
-            out = torch.empty((M, heads, D), dtype=torch.bfloat16, device=t.device)
-        oheads, orow, ohead = _heads(out, M, D, "out_" + name)
-        if oheads != heads:
-            raise ValueError(f"out_{name} must have {heads} heads, got {oheads}")
-        if w is not None:
-            _require(w, torch.bfloat16, (D,), "norm_w" + name)
-        args.append((_ptr(t), row, head, heads, _ptr(out), orow, ohead, _ptr(w)))
+            out = t.new_empty((M, heads, D))
+            op, orow, ohead = out.data_ptr(), heads * D, D
+        else:
+            op, orow, ohead, oheads = _heads(out, M, D, "out_" + name, dev)
+            if oheads != heads:
+                raise ValueError(f"out_{name} must have {heads} heads, got {oheads}")
+        wp = _addr(w, torch.bfloat16, (D,), "norm_w" + name, dev) if w is not None else None
+        views.append((tp, row, head, heads, op, orow, ohead, wp))
         outs.append(out)
-    (qp, qr, qh, nq, oqp, oqr, oqh, wq), (kp, kr, kh, nk, okp, okr, okh, wk) = args
-    st = LIB.svdq_qk_norm_rope(qp, qr, qh, nq, kp, kr, kh, nk, M, D, wq, wk, float(eps), _ptr(positions), is_float, P,
-                               axes, dims, thetas, _PAIRINGS[pairing], oqp, oqr, oqh, okp, okr, okh, _stream())
-    _check("svdq_qk_norm_rope", st)
+    (qp, qr, qh, nq, oqp, oqr, oqh, wq), (kp, kr, kh, nk, okp, okr, okh, wk) = views
+    st = LIB.svdq_qk_norm_rope(qp, qr, qh, nq, kp, kr, kh, nk, M, D, wq, wk, eps, positions.data_ptr(), is_float, P,
+                               axes, dims, thetas, _PAIRINGS[pairing], oqp, oqr, oqh, okp, okr, okh,
+                               torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check("svdq_qk_norm_rope", st)
     return tuple(outs)
 
 
 def svdq_rope_axes_tables(positions, axes_dims, theta, head_dim, rows=None, rope_cos=None, rope_sin=None):
     """The (cos, sin) tables, float32 [head_dim / 2, rows], of positions with several axes, in the layout
     of svdq_w4a4_nvfp4_linear_qkv; arguments as svdq_qk_norm_rope (rows: a multiple of P, by default P)."""
-    P, axes, is_float, dims, thetas = _rope_axes(positions, axes_dims, theta)
+    dev, P, axes, is_float, dims, thetas = _rope_axes(positions, axes_dims, theta)
     M = P if rows is None else rows
     shape = (head_dim // 2, M)
     if rope_cos is None:
         rope_cos = torch.empty(shape, dtype=torch.float32, device=positions.device)
     if rope_sin is None:
         rope_sin = torch.empty(shape, dtype=torch.float32, device=positions.device)
-    _require(rope_cos, torch.float32, shape, "rope_cos")
-    _require(rope_sin, torch.float32, shape, "rope_sin")
-    st = LIB.svdq_rope_axes_tables(_ptr(positions), is_float, P, axes, dims, thetas, M, head_dim, _ptr(rope_cos),
-                                   _ptr(rope_sin), _stream())
-    _check("svdq_rope_axes_tables", st)
+    cp = _addr(rope_cos, torch.float32, shape, "rope_cos", dev)
+    sp = _addr(rope_sin, torch.float32, shape, "rope_sin", dev)
+    st = LIB.svdq_rope_axes_tables(positions.data_ptr(), is_float, P, axes, dims, thetas, M, head_dim, cp, sp,
+                                   torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check("svdq_rope_axes_tables", st)
     return rope_cos, rope_sin
 
 
