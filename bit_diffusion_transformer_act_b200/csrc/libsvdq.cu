@@ -5,6 +5,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <string.h>
+
 #include <algorithm>
 #include <atomic>
 #include <numeric>
@@ -1105,24 +1107,31 @@ int svdq_lora_add(const void* X, int64_t ldx, const void* Yin, int64_t ldyin, co
   return launch_status();
 }
 
-// The pairs' frequencies in turns per unit of position.  Along an axis they are a geometric sequence; with 64-bit products the last of 128 is off by
-// at most 128 * 2^-53, as far as the position's product itself at 2^7 turns.
-static void rope_freqs(int axes, const int32_t* dims, const double* theta, svdq::k9::Freqs* fr, int* rot) {
+// The pairs' frequencies in turns per unit of position, as the kernels read them (see Freqs); returns the
+// rotated width.  Along an axis they are a geometric sequence, formed in extended precision (128 products
+// of 2^-64 each).
+static int rope_freqs(int axes, const int32_t* dims, const double* theta, bool is_float, svdq::k9::Freqs* fr) {
   int at = 0;
   for (int a = 0; a < axes; ++a) {
-    const double ratio = std::pow(theta[a], -2.0 / dims[a]);
-    double f = 0.15915494309189533577;             // 1 / (2 pi)
+    const long double ratio = std::pow(static_cast<long double>(theta[a]), -2.0L / dims[a]);
+    long double f = 0.159154943091895335768883763372514362L;   // 1 / (2 pi)
     for (int i = 0; i < dims[a] / 2; ++i, ++at) {
-      fr->f[at] = f;
+      if (is_float) {
+        const double d = static_cast<double>(f);
+        memcpy(&fr->f[at], &d, sizeof(d));
+      } else {
+        fr->f[at] = static_cast<uint64_t>(std::ldexp(f - std::floor(f), 64));   // whole turns do not count
+      }
       fr->axis[at] = static_cast<uint8_t>(a);
       f *= ratio;
     }
   }
-  *rot = 2 * at;
+  const int rot = 2 * at;
   for (; at < svdq::k9::kMaxPairs; ++at) {
-    fr->f[at] = 0.0;
+    fr->f[at] = 0;
     fr->axis[at] = 0;
   }
+  return rot;
 }
 
 // Checks of the arguments that both rotary calls share.
@@ -1203,7 +1212,7 @@ int svdq_qk_norm_rope(const void* Q, int64_t q_row_stride, int64_t q_head_stride
   namespace k9 = svdq::k9;
   k9::Freqs fr;
   k9::Params p;
-  rope_freqs(axes, axis_dims, axis_theta, &fr, &p.rot);
+  p.rot = rope_freqs(axes, axis_dims, axis_theta, positions_float != 0, &fr);
   auto view = [](const HeadsView& v) {
     return k9::View{static_cast<__nv_bfloat16*>(const_cast<void*>(v.ptr)), v.row, v.head};
   };
@@ -1214,7 +1223,6 @@ int svdq_qk_norm_rope(const void* Q, int64_t q_row_stride, int64_t q_head_stride
   p.wq = static_cast<const __nv_bfloat16*>(norm_wq);
   p.wk = static_cast<const __nv_bfloat16*>(norm_wk);
   p.pos = positions;
-  p.pos_float = positions_float != 0;
   p.axes = axes;
   p.P = P;
   p.M = M;
@@ -1233,11 +1241,15 @@ int svdq_qk_norm_rope(const void* Q, int64_t q_row_stride, int64_t q_head_stride
   while (p.parts < 8 && 2 * p.parts <= passes && M * 2ll * p.parts <= most) p.parts *= 2;
   const int64_t blocks = (static_cast<int64_t>(M) * p.parts + k9::kThreads / 32 - 1) / (k9::kThreads / 32);
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(k9::kBlocksPerSm) * sm_count(dev))));
-#define SVDQ_ROPE_CASE(V_, L_)                                                                                  \
-  if (V == V_ && lpr == L_)                                                                                     \
-    return launch_pdl(pairing ? k9::qk_norm_rope_kernel<V_, L_, true> : k9::qk_norm_rope_kernel<V_, L_, false>, \
-                      grid, k9::kThreads, 0, 1, stream, p, fr)                                                     \
-               ? launch_status()                                                                                \
+  const int kind = (pairing ? 2 : 0) + (positions_float ? 1 : 0);
+#define SVDQ_ROPE_CASE(V_, L_)                                                                            \
+  if (V == V_ && lpr == L_)                                                                               \
+    return launch_pdl(kind == 0   ? k9::qk_norm_rope_kernel<V_, L_, false, false>                         \
+                      : kind == 1 ? k9::qk_norm_rope_kernel<V_, L_, false, true>                          \
+                      : kind == 2 ? k9::qk_norm_rope_kernel<V_, L_, true, false>                          \
+                                  : k9::qk_norm_rope_kernel<V_, L_, true, true>,                          \
+                      grid, k9::kThreads, 0, 1, stream, p, fr)                                            \
+               ? launch_status()                                                                          \
                : SVDQ_ERR_CUDA
   SVDQ_ROPE_CASE(8, 1);
   SVDQ_ROPE_CASE(8, 2);
@@ -1266,10 +1278,8 @@ int svdq_rope_axes_tables(const void* positions, int positions_float, int P, int
   namespace k9 = svdq::k9;
   k9::Freqs fr;
   k9::TableParams p;
-  int rot = 0;
-  rope_freqs(axes, axis_dims, axis_theta, &fr, &rot);
+  const int rot = rope_freqs(axes, axis_dims, axis_theta, positions_float != 0, &fr);
   p.pos = positions;
-  p.pos_float = positions_float != 0;
   p.axes = axes;
   p.P = P;
   p.M = M;
@@ -1281,7 +1291,7 @@ int svdq_rope_axes_tables(const void* positions, int positions_float, int P, int
   // pairs per thread: the fewest that keep the grid within eight blocks per SM
   const int by = std::max(1, std::min(p.pairs, 8 * sm_count(dev) / bx));
   p.per = (p.pairs + by - 1) / by;
-  if (!launch_pdl(k9::rope_tables_kernel, dim3(bx, (p.pairs + p.per - 1) / p.per), k9::kThreads, 0, 1, stream, p, fr))
+  if (!launch_pdl(positions_float ? k9::rope_tables_kernel<true> : k9::rope_tables_kernel<false>, dim3(bx, (p.pairs + p.per - 1) / p.per), k9::kThreads, 0, 1, stream, p, fr))
     return SVDQ_ERR_CUDA;
   return launch_status();
 }

@@ -3,12 +3,17 @@
 // (kernel 10).
 //
 // Mathematics.  A head's rotary pairs are dealt to the axes in order (axis a has d_a / 2 pairs);
-// pair i of axis a turns by position[m, a] * theta_a^(-2 i / d_a).  The host passes each pair's
-// frequency in turns, f = theta_a^(-2 i / d_a) / (2 pi), in 64 bits; the kernel forms
-// t = position * f in 64 bits, subtracts the nearest integer, and takes the sine and cosine of
-// 2 pi (t - rint t) in 32 bits.  A product in 32 bits would be off by position * 2^-24 radians
-// (0.004 at position 65536); here the angle is within 2^-52 |t| turns before its one rounding
-// to 32 bits.
+// pair i of axis a turns by position[m, a] * theta_a^(-2 i / d_a).  Only the angle's fraction of a
+// turn counts, so the host passes each pair's frequency in turns, f = theta_a^(-2 i / d_a) / (2 pi), and the
+// kernels form the fraction in units of 2^-32 turns:
+//   - integer positions: f as a 64-bit fixed-point fraction; position * f modulo one turn is the
+//     product modulo 2^64, of which the upper half is kept -- exact but for f's own rounding (2^-64);
+//   - float positions: position * f in 64-bit floating point, less the nearest integer.
+// (A product in 32 bits would be off by position * 2^-24 radians: 0.004 at position 65536.)  The fraction's
+// upper two bits, rounded, are the quarter; the rest is an angle within pi / 4, exact to 2^-24 of itself
+// as a float, whose sine and cosine are the Taylor polynomials of degree 9 and 8: their remainders are at
+// most x^11 / 11! < 2^-29 and x^10 / 10! < 2^-25 there.  Thus 28 instructions per pair, where the 64-bit
+// reduction and the library's sine and cosine of any argument took about 100.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -26,7 +31,8 @@ constexpr int kThreads = 256;
 constexpr int kBlocksPerSm = 3;
 
 struct Freqs {
-  double f[kMaxPairs];                     // turns per unit of position, in pair order
+  uint64_t f[kMaxPairs];                   // turns per unit of position, in pair order: for integer positions the
+                                           // fraction in units of 2^-64, for float ones the bits of a double
   uint8_t axis[kMaxPairs];
 };
 
@@ -39,21 +45,46 @@ struct Params {
   View q, k, oq, ok;
   const __nv_bfloat16 *wq, *wk;            // [D] or null (no normalisation)
   const void* pos;                         // [P, axes] int32, or float32
-  int pos_float;
   int axes, P, M, q_heads, k_heads;
   int D, rot;                              // head width, rotated columns
   int parts;                               // warps that share a token's heads
   float eps;
 };
 
-__device__ __forceinline__ double position(const void* pos, int is_float, long long i) {
-  return is_float ? static_cast<double>(__ldg(static_cast<const float*>(pos) + i))
-                  : static_cast<double>(__ldg(static_cast<const int*>(pos) + i));
+// The angle of one position and frequency, in 2^-32 turns.
+template <bool kFloat>
+__device__ __forceinline__ uint32_t turn_fraction(uint32_t pos_bits, uint64_t f) {
+  if constexpr (kFloat) {
+    const double t = static_cast<double>(__uint_as_float(pos_bits)) * __longlong_as_double(static_cast<long long>(f));
+    // adding 1.5 * 2^20 to the fraction leaves it in units of 2^-32 in the low half of the result
+    return static_cast<uint32_t>(__double2loint(t - rint(t) + 1572864.0));
+  } else {
+    const int p = static_cast<int>(pos_bits);
+    const uint32_t hi = static_cast<uint32_t>(f >> 32), lo = static_cast<uint32_t>(f);
+    // upper half of p * f modulo 2^64 (p < 0: its unsigned value less 2^32, whose product with f's low
+    // half comes back off the upper half)
+    return static_cast<uint32_t>(p) * hi + __umulhi(static_cast<uint32_t>(p), lo) - (p < 0 ? lo : 0u);
+  }
 }
 
-// Sine and cosine of `turns` turns.
-__device__ __forceinline__ void sincos_turns(double turns, float& s, float& c) {
-  sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &s, &c);
+// Sine and cosine of `frac` * 2^-32 turns.
+__device__ __forceinline__ void sincos_turns(uint32_t frac, float& s, float& c) {
+  const uint32_t q = (frac + 0x20000000u) >> 30;   // nearest quarter turn
+  const float x = static_cast<float>(static_cast<int>(frac - (q << 30))) * 1.46291807926715968e-9f;   // 2 pi 2^-32
+  const float z = x * x;
+  const float sp = fmaf(fmaf(fmaf(fmaf(1.f / 362880.f, z, -1.f / 5040.f), z, 1.f / 120.f), z, -1.f / 6.f) * z, x, x);
+  const float cp = fmaf(fmaf(fmaf(fmaf(1.f / 40320.f, z, -1.f / 720.f), z, 1.f / 24.f), z, -0.5f), z, 1.f);
+  const float a = q & 1u ? cp : sp, b = q & 1u ? sp : cp;
+  s = __uint_as_float(__float_as_uint(a) ^ ((q & 2u) << 30));
+  c = __uint_as_float(__float_as_uint(b) ^ (((q + 1u) & 2u) << 30));
+}
+
+// The position's bits; a float position that is not finite has no angle: `bad` is NaN for it, else 0.
+template <bool kFloat>
+__device__ __forceinline__ uint32_t position(const void* pos, long long i, float& bad) {
+  const uint32_t bits = __ldg(static_cast<const uint32_t*>(pos) + i);
+  bad = kFloat ? __uint_as_float(bits) * 0.f : 0.f;
+  return bits;
 }
 
 template <int V>
@@ -82,7 +113,7 @@ __device__ __forceinline__ void store_v(__nv_bfloat16* p, const uint32_t (&r)[V 
 // Bound by memory (q and k read and written once: 4 bytes a value) if the instructions are few: with the
 // sines formed by every lane, the weights unpacked per head and scalar arithmetic the kernel issued
 // 2940 warp instructions per token of 40 heads and took 61 us at 9216 tokens (floor 29 us).
-template <int V, int LPR, bool kHalf>
+template <int V, int LPR, bool kHalf, bool kFloat>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 qk_norm_rope_kernel(const __grid_constant__ Params p, const __grid_constant__ Freqs fr) {
   constexpr int HPW = 32 / LPR;
@@ -93,12 +124,12 @@ qk_norm_rope_kernel(const __grid_constant__ Params p, const __grid_constant__ Fr
   const bool turned = u * 2 * V < p.rot;           // units past the rotated columns are only normalised
   const int e0 = turned && kHalf ? V * u : 2 * V * u;
   const int run = turned && kHalf ? p.rot / 2 : V;  // from the unit's first run to its second
-  double f[kShare];
+  uint64_t f[kShare];
   int ax[kShare];
 #pragma unroll
   for (int j = 0; j < kShare; ++j) {
     const int i = V * u + sub * kShare + j;        // (lanes with sub >= V have nothing to form)
-    f[j] = turned && sub * kShare < V ? fr.f[i] : 0.0;
+    f[j] = turned && sub * kShare < V ? fr.f[i] : 0u;
     ax[j] = turned && sub * kShare < V ? fr.axis[i] : 0;
   }
   grid_dependency_wait();                          // q and k come from the previous kernel
@@ -113,7 +144,15 @@ qk_norm_rope_kernel(const __grid_constant__ Params p, const __grid_constant__ Fr
     float cs[kShare], sn[kShare];
     const long long at = static_cast<long long>(static_cast<int>(m) % p.P) * p.axes;
 #pragma unroll
-    for (int j = 0; j < kShare; ++j) sincos_turns(position(p.pos, p.pos_float, at + ax[j]) * f[j], sn[j], cs[j]);
+    for (int j = 0; j < kShare; ++j) {
+      float bad;
+      const uint32_t x = position<kFloat>(p.pos, at + ax[j], bad);
+      sincos_turns(turn_fraction<kFloat>(x, f[j]), sn[j], cs[j]);
+      if (kFloat) {
+        sn[j] += bad;
+        cs[j] += bad;
+      }
+    }
     // This lane's heads of q or of k: written twice into the code, so that the strides and pointers stay
     // operands from the parameters instead of selected values.
     auto rotate = [&](const View& vi, const View& vo, const __nv_bfloat16* w, int heads) {
@@ -243,12 +282,12 @@ qk_norm_rope_kernel(const __grid_constant__ Params p, const __grid_constant__ Fr
 // m + 2P, ... have the same position and get the same values.
 struct TableParams {
   const void* pos;
-  int pos_float;
   int axes, P, M, pairs, rot_pairs;
   int per;                                 // pairs per grid row
   float *cos, *sin;                        // [pairs, M]
 };
 
+template <bool kFloat>
 __global__ void __launch_bounds__(kThreads)
 rope_tables_kernel(const __grid_constant__ TableParams p, const __grid_constant__ Freqs fr) {
   grid_dependency_wait();
@@ -256,23 +295,38 @@ rope_tables_kernel(const __grid_constant__ TableParams p, const __grid_constant_
   const int m0 = blockIdx.x * kThreads + threadIdx.x;
   if (m0 >= p.P) return;
   const int i0 = blockIdx.y * p.per, i1 = min(i0 + p.per, p.pairs);
-  int last = -1;
-  double x = 0.0;
-  for (int i = i0; i < i1; ++i) {
-    float s = 0.f, c = 1.f;                        // pairs past the rotated columns stay as they are
-    if (i < p.rot_pairs) {
-      const int a = fr.axis[i];
-      if (a != last) {
-        x = position(p.pos, p.pos_float, static_cast<long long>(m0) * p.axes + a);
-        last = a;
+  float* cos = p.cos + static_cast<long long>(i0) * p.M + m0;
+  float* sin = p.sin + static_cast<long long>(i0) * p.M + m0;
+  int i = i0;
+  while (i < min(i1, p.rot_pairs)) {               // axis by axis
+    const int a = fr.axis[i];
+    float bad;
+    const uint32_t x = position<kFloat>(p.pos, static_cast<long long>(m0) * p.axes + a, bad);
+    int end = i + 1;
+    while (end < min(i1, p.rot_pairs) && fr.axis[end] == a) ++end;
+#pragma unroll 4
+    for (; i < end; ++i) {
+      float s, c;
+      sincos_turns(turn_fraction<kFloat>(x, fr.f[i]), s, c);
+      if (kFloat) {
+        s += bad;
+        c += bad;
       }
-      sincos_turns(x * fr.f[i], s, c);
-    }
-    for (long long m = m0; m < p.M; m += p.P) {
-      p.cos[static_cast<long long>(i) * p.M + m] = c;
-      p.sin[static_cast<long long>(i) * p.M + m] = s;
+      cos[0] = c;
+      sin[0] = s;
+      for (long long m = p.P; m < p.M - m0; m += p.P) {
+        cos[m] = c;
+        sin[m] = s;
+      }
+      cos += p.M;
+      sin += p.M;
     }
   }
+  for (; i < i1; ++i, cos += p.M, sin += p.M)      // pairs past the rotated columns stay as they are
+    for (long long m = 0; m < p.M - m0; m += p.P) {
+      cos[m] = 1.f;
+      sin[m] = 0.f;
+    }
 }
 
 }  // namespace k9

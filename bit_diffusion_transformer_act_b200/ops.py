@@ -7,6 +7,7 @@ is not sm_100 the calls raise.
 """
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -646,6 +647,15 @@ def svdq_lora_add(X, Y, A, B, plan, out=None, workspace=None):
     return out
 
 
+@functools.lru_cache(maxsize=64)
+def _axes_arrays(dims, theta):
+    """The ctypes arrays of axes of these widths (a tuple) and thetas (one, or a tuple)."""
+    thetas = theta if isinstance(theta, tuple) else (theta,) * len(dims)
+    if len(thetas) != len(dims):
+        raise ValueError(f"{len(dims)} axes need one theta or {len(dims)}")
+    return (ctypes.c_int32 * len(dims))(*dims), (ctypes.c_double * len(dims))(*thetas)
+
+
 def _rope_axes(positions, axes_dims, theta):
     """Checked positions and the ctypes arrays of the axes: (device, P, axes, is_float, dims, thetas)."""
     is_float = isinstance(positions, torch.Tensor) and positions.dtype is torch.float32
@@ -656,10 +666,10 @@ def _rope_axes(positions, axes_dims, theta):
     if positions.get_device() != dev or dev < 0:
         _on_device(positions, "positions")
     P, axes = positions.shape
-    thetas = [theta] * axes if isinstance(theta, (int, float)) else theta
-    if len(axes_dims) != axes or len(thetas) != axes:
-        raise ValueError(f"{axes} axes need {axes} widths and one theta or {axes}")
-    return dev, P, axes, int(is_float), (ctypes.c_int32 * axes)(*axes_dims), (ctypes.c_double * axes)(*thetas)
+    if len(axes_dims) != axes:
+        raise ValueError(f"{axes} axes need {axes} widths, got {len(axes_dims)}")
+    dims, thetas = _axes_arrays(tuple(axes_dims), tuple(theta) if isinstance(theta, (list, tuple)) else theta)
+    return dev, P, axes, int(is_float), dims, thetas
 
 
 _PAIRINGS = {"interleaved": 0, "half": 1}
@@ -727,12 +737,14 @@ def svdq_rope_axes_tables(positions, axes_dims, theta, head_dim, rows=None, rope
     dev, P, axes, is_float, dims, thetas = _rope_axes(positions, axes_dims, theta)
     M = P if rows is None else rows
     shape = (head_dim // 2, M)
-    if rope_cos is None:
-        rope_cos = torch.empty(shape, dtype=torch.float32, device=positions.device)
-    if rope_sin is None:
-        rope_sin = torch.empty(shape, dtype=torch.float32, device=positions.device)
-    cp = _addr(rope_cos, torch.float32, shape, "rope_cos", dev)
-    sp = _addr(rope_sin, torch.float32, shape, "rope_sin", dev)
+    tables = []
+    for t, name in ((rope_cos, "rope_cos"), (rope_sin, "rope_sin")):
+        if t is None:
+            t = positions.new_empty(shape, dtype=torch.float32)
+            tables.append((t, t.data_ptr()))
+        else:
+            tables.append((t, _addr(t, torch.float32, shape, name, dev)))
+    (rope_cos, cp), (rope_sin, sp) = tables
     st = LIB.svdq_rope_axes_tables(positions.data_ptr(), is_float, P, axes, dims, thetas, M, head_dim, cp, sp,
                                    torch._C._cuda_getCurrentRawStream(dev))
     if st:
