@@ -1234,23 +1234,37 @@ int svdq_qk_norm_rope(const void* Q, int64_t q_row_stride, int64_t q_head_stride
   const int V = D % 16 == 0 && p.rot % 16 == 0 ? 8 : 4;
   int lpr = 1;
   while (lpr * 2 * V < D) lpr *= 2;
-  // warps per token: as many as the token's heads can use while the grid has fewer than 16 per SM
-  const int passes = (std::max(q_heads, k_heads) + 32 / lpr - 1) / (32 / lpr);
-  const int64_t most = 16ll * sm_count(dev);
-  p.parts = 1;
-  while (p.parts < 8 && 2 * p.parts <= passes && M * 2ll * p.parts <= most) p.parts *= 2;
-  const int64_t blocks = (static_cast<int64_t>(M) * p.parts + k9::kThreads / 32 - 1) / (k9::kThreads / 32);
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(k9::kBlocksPerSm) * sm_count(dev))));
+  // Groups of heads (what a warp holds at once) per unit: all of a token's, fewer where a unit would exceed
+  // kUnitBytes (so that every warp has two stages), and fewer while there are less than two units for every warp
+  // of the device.
+  const int hpw = 32 / lpr;
+  p.q_groups = (q_heads + hpw - 1) / hpw;
+  p.groups = p.q_groups + (k_heads + hpw - 1) / hpw;
+  const int group_bytes = hpw * D * 2;               // at most 1 KB
+  const int64_t warps = static_cast<int64_t>(k9::kBlocksPerSm) * sm_count(dev) * k9::kWarps;
+  const int64_t least = std::max<int64_t>((p.groups + k9::kUnitBytes / group_bytes - 1) / (k9::kUnitBytes / group_bytes),
+                                          std::min<int64_t>(p.groups, 2 * warps / M));
+  p.chunk = static_cast<int>((p.groups + least - 1) / std::max<int64_t>(1, least));
+  p.units = static_cast<uint32_t>((p.groups + p.chunk - 1) / p.chunk);
+  if (static_cast<int64_t>(M) * p.units > INT32_MAX) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  p.stage_bytes = (p.chunk * group_bytes + 127) / 128 * 128;
+  p.stage_log = 4;
+  static_assert(2 * k9::kWarps == 1 << 4, "the least stage_log");
+  while ((2 << p.stage_log) <= k9::kMaxStages && (2 << p.stage_log) * p.stage_bytes <= k9::kRingBytes) ++p.stage_log;
+  const int smem = (p.stage_bytes << p.stage_log) + k9::kAfterBytes;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(M) * p.units, static_cast<int64_t>(k9::kBlocksPerSm) * sm_count(dev))));
   const int kind = (pairing ? 2 : 0) + (positions_float ? 1 : 0);
+#define SVDQ_ROPE_LAUNCH(V_, L_, H_, F_)                                                               \
+  (set_smem_once<k9::qk_norm_rope_kernel<V_, L_, H_, F_>>(k9::kRingBytes + k9::kAfterBytes, dev) &&         \
+           launch_pdl(k9::qk_norm_rope_kernel<V_, L_, H_, F_>, grid, k9::kThreads, smem, 1, stream, p, fr) \
+       ? launch_status()                                                                                  \
+       : SVDQ_ERR_CUDA)
 #define SVDQ_ROPE_CASE(V_, L_)                                                                            \
   if (V == V_ && lpr == L_)                                                                               \
-    return launch_pdl(kind == 0   ? k9::qk_norm_rope_kernel<V_, L_, false, false>                         \
-                      : kind == 1 ? k9::qk_norm_rope_kernel<V_, L_, false, true>                          \
-                      : kind == 2 ? k9::qk_norm_rope_kernel<V_, L_, true, false>                          \
-                                  : k9::qk_norm_rope_kernel<V_, L_, true, true>,                          \
-                      grid, k9::kThreads, 0, 1, stream, p, fr)                                            \
-               ? launch_status()                                                                          \
-               : SVDQ_ERR_CUDA
+    return kind == 0   ? SVDQ_ROPE_LAUNCH(V_, L_, false, false)                                           \
+           : kind == 1 ? SVDQ_ROPE_LAUNCH(V_, L_, false, true)                                            \
+           : kind == 2 ? SVDQ_ROPE_LAUNCH(V_, L_, true, false)                                            \
+                       : SVDQ_ROPE_LAUNCH(V_, L_, true, true)
   SVDQ_ROPE_CASE(8, 1);
   SVDQ_ROPE_CASE(8, 2);
   SVDQ_ROPE_CASE(8, 4);
@@ -1263,6 +1277,7 @@ int svdq_qk_norm_rope(const void* Q, int64_t q_row_stride, int64_t q_head_stride
   SVDQ_ROPE_CASE(4, 16);
   SVDQ_ROPE_CASE(4, 32);
 #undef SVDQ_ROPE_CASE
+#undef SVDQ_ROPE_LAUNCH
   return SVDQ_ERR_UNSUPPORTED_SHAPE;
 }
 
@@ -1287,11 +1302,11 @@ int svdq_rope_axes_tables(const void* positions, int positions_float, int P, int
   p.rot_pairs = rot / 2;
   p.cos = static_cast<float*>(rope_cos);
   p.sin = static_cast<float*>(rope_sin);
-  const int bx = (P + k9::kThreads - 1) / k9::kThreads;
+  const int bx = (P + k9::kTableThreads - 1) / k9::kTableThreads;
   // pairs per thread: the fewest that keep the grid within eight blocks per SM
   const int by = std::max(1, std::min(p.pairs, 8 * sm_count(dev) / bx));
   p.per = (p.pairs + by - 1) / by;
-  if (!launch_pdl(positions_float ? k9::rope_tables_kernel<true> : k9::rope_tables_kernel<false>, dim3(bx, (p.pairs + p.per - 1) / p.per), k9::kThreads, 0, 1, stream, p, fr))
+  if (!launch_pdl(positions_float ? k9::rope_tables_kernel<true> : k9::rope_tables_kernel<false>, dim3(bx, (p.pairs + p.per - 1) / p.per), k9::kTableThreads, 0, 1, stream, p, fr))
     return SVDQ_ERR_CUDA;
   return launch_status();
 }

@@ -328,12 +328,17 @@ lora_tile_up_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
     for (int i = i0; i < i1; ++i, ++it) {
       const int t = i / p.chunks;
       const int s = it % S;
-      if (t >= p.ntiles) {                          // a copied piece: no MMA reads this stage
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(full(s), (it / S) & 1u, abort_flag, 83))) break;
-        if (lane == 0) mbar_arrive(empty(s));
+      const int b = it % kGroups;
+      if (t >= p.ntiles) {                          // a copied piece: handed on in its turn, without an MMA
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(full(s), (it / S) & 1u, abort_flag, 83) &&
+                                         mbar_wait_bounded(acc_empty(b), ((it / kGroups) & 1u) ^ 1u, abort_flag, 90)))
+          break;
+        if (lane == 0) {
+          mbar_arrive(acc_full(b));
+          mbar_arrive(empty(s));
+        }
         continue;
       }
-      const int b = it % kGroups;                   // copied pieces come last, so this counts MMA pieces
       bool ok = true;
       if (t != last) {
         ok = mbar_wait_bounded(u_full(nu & 1), (nu >> 1) & 1u, abort_flag, 84);
@@ -435,8 +440,11 @@ lora_tile_up_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
       if (t != last) tile = tile_of(t);
       last = t;
       const bool busy = t < p.ntiles;
-      bool ok = mbar_wait_bounded(full(s), (it / S) & 1u, abort_flag, 87);
-      if (busy) ok = ok && mbar_wait_bounded(acc_full(b), (it / kGroups) & 1u, abort_flag, 88);
+      // The accumulator first: pieces are handed over in order, so this piece's stage is then in its own phase.
+      // (The other order could take an earlier phase's end for this one's, where the stage was last used by
+      // the other group.)
+      const bool ok = mbar_wait_bounded(acc_full(b), (it / kGroups) & 1u, abort_flag, 87) &&
+                      mbar_wait_bounded(full(s), (it / S) & 1u, abort_flag, 88);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc_fence_after();
       const int rows = min(32, tile.y - 32 * q);    // of this slab; none or fewer where the tile ends
@@ -468,11 +476,9 @@ lora_tile_up_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
           }
         }
       }
-      if (busy) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty(b));   // the accumulator has been read
-      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty(b));     // the accumulator has been read
       if (rows == 32) {
         fence_proxy_async_smem();
         __syncwarp();
