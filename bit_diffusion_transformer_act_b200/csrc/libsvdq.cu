@@ -1302,7 +1302,7 @@ int svdq_rope_axes_tables(const void* positions, int positions_float, int P, int
   p.rot_pairs = rot / 2;
   p.cos = static_cast<float*>(rope_cos);
   p.sin = static_cast<float*>(rope_sin);
-  const int bx = (P + k9::kTableThreads - 1) / k9::kTableThreads;
+  const int bx = (P - 1) / (k9::kTableThreads * k9::kTokens) + 1;
   // pairs per thread: the fewest that keep the grid within eight blocks per SM
   const int by = std::max(1, std::min(p.pairs, 8 * sm_count(dev) / bx));
   p.per = (p.pairs + by - 1) / by;

@@ -20,6 +20,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "ptx.cuh"
 
 namespace svdq {
@@ -62,26 +64,26 @@ struct Params {
   float eps;
 };
 
-// The angle of one position and frequency, in 2^-32 turns.
 template <bool kFloat>
-__device__ __forceinline__ uint32_t turn_fraction(uint32_t pos_bits, uint64_t f) {
-  if constexpr (kFloat) {
-    const double t = static_cast<double>(__uint_as_float(pos_bits)) * __longlong_as_double(static_cast<long long>(f));
-    // adding 1.5 * 2^20 to the fraction leaves it in units of 2^-32 in the low half of the result
-    return static_cast<uint32_t>(__double2loint(t - rint(t) + 1572864.0));
-  } else {
-    const int p = static_cast<int>(pos_bits);
-    const uint32_t hi = static_cast<uint32_t>(f >> 32), lo = static_cast<uint32_t>(f);
-    // upper half of p * f modulo 2^64 (p < 0: its unsigned value less 2^32, whose product with f's low
-    // half comes back off the upper half)
-    return static_cast<uint32_t>(p) * hi + __umulhi(static_cast<uint32_t>(p), lo) - (p < 0 ? lo : 0u);
-  }
+using Position = std::conditional_t<kFloat, double, int>;
+
+// The angle of one position and frequency, in 2^-32 turns.
+__device__ __forceinline__ uint32_t turn_fraction(double pos, uint64_t f) {
+  const double t = pos * __longlong_as_double(static_cast<long long>(f));
+  // adding 1.5 * 2^20 to the fraction leaves it in units of 2^-32 in the low half of the result
+  return static_cast<uint32_t>(__double2loint(t - rint(t) + 1572864.0));
+}
+__device__ __forceinline__ uint32_t turn_fraction(int pos, uint64_t f) {
+  const uint32_t p = static_cast<uint32_t>(pos), hi = static_cast<uint32_t>(f >> 32), lo = static_cast<uint32_t>(f);
+  // upper half of pos * f modulo 2^64 (pos < 0: its unsigned value less 2^32, whose product with f's low
+  // half comes back off the upper half)
+  return p * hi + __umulhi(p, lo) - (pos < 0 ? lo : 0u);
 }
 
-// Sine and cosine of `frac` * 2^-32 turns.
-__device__ __forceinline__ void sincos_turns(uint32_t frac, float& s, float& c) {
+// Sine and cosine of `frac` * 2^-32 turns; NaN where `bad` is (else it is 0).
+__device__ __forceinline__ void sincos_turns(uint32_t frac, float bad, float& s, float& c) {
   const uint32_t q = (frac + 0x20000000u) >> 30;   // nearest quarter turn
-  const float x = static_cast<float>(static_cast<int>(frac - (q << 30))) * 1.46291807926715968e-9f;   // 2 pi 2^-32
+  const float x = fmaf(static_cast<float>(static_cast<int>(frac - (q << 30))), 1.46291807926715968e-9f, bad);   // 2 pi 2^-32
   const float z = x * x;
   const float sp = fmaf(fmaf(fmaf(fmaf(1.f / 362880.f, z, -1.f / 5040.f), z, 1.f / 120.f), z, -1.f / 6.f) * z, x, x);
   const float cp = fmaf(fmaf(fmaf(fmaf(1.f / 40320.f, z, -1.f / 720.f), z, 1.f / 24.f), z, -0.5f), z, 1.f);
@@ -90,12 +92,17 @@ __device__ __forceinline__ void sincos_turns(uint32_t frac, float& s, float& c) 
   c = __uint_as_float(__float_as_uint(b) ^ (((q + 1u) & 2u) << 30));
 }
 
-// The position's bits; a float position that is not finite has no angle: `bad` is NaN for it, else 0.
+// A position; a float one that is not finite has no angle: `bad` is NaN for it, else 0.
 template <bool kFloat>
-__device__ __forceinline__ uint32_t position(const void* pos, long long i, float& bad) {
-  const uint32_t bits = __ldg(static_cast<const uint32_t*>(pos) + i);
-  bad = kFloat ? __uint_as_float(bits) * 0.f : 0.f;
-  return bits;
+__device__ __forceinline__ Position<kFloat> position(const void* pos, long long i, float& bad) {
+  if constexpr (kFloat) {
+    const float x = __ldg(static_cast<const float*>(pos) + i);
+    bad = x * 0.f;
+    return static_cast<double>(x);
+  } else {
+    bad = 0.f;
+    return __ldg(static_cast<const int*>(pos) + i);
+  }
 }
 
 template <int V>
@@ -246,7 +253,7 @@ qk_norm_rope_kernel(const __grid_constant__ Params p, const __grid_constant__ Fr
       const __nv_bfloat16* w = i < p.D ? p.wq : p.wk;
       weights[i] = w ? w[i < p.D ? i : i - p.D] : __float2bfloat16_rn(1.f);
     }
-    uint32_t pos[kShare];
+    Position<kFloat> pos[kShare];
     float bad[kShare];
     auto fetch_position = [&](uint32_t w) {
       uint32_t m = p.units > 1 ? w / p.units : w;
@@ -265,11 +272,7 @@ qk_norm_rope_kernel(const __grid_constant__ Params p, const __grid_constant__ Fr
       float cs[kShare], sn[kShare];
 #pragma unroll
       for (int j = 0; j < kShare; ++j) {
-        sincos_turns(turn_fraction<kFloat>(pos[j], f[j]), sn[j], cs[j]);
-        if (kFloat) {
-          sn[j] += bad[j];
-          cs[j] += bad[j];
-        }
+        sincos_turns(turn_fraction(pos[j], f[j]), bad[j], sn[j], cs[j]);
       }
       if (n + kWarps < count) fetch_position(w0 + (n + kWarps) * step);   // the next unit's, while this one is worked on
       if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(full(s), (n >> p.stage_log) & 1u, abort_flag, 92))) break;
@@ -399,9 +402,12 @@ qk_norm_rope_kernel(const __grid_constant__ Params p, const __grid_constant__ Fr
   }
 }
 
-// Kernel 10: a thread owns one position (a column of the tables) and walks over a share of the
-// pairs; 32 neighbouring threads write one 128-byte line of each table.  Tokens m, m + P,
-// m + 2P, ... have the same position and get the same values.
+// Kernel 10: a thread owns kTokens positions (columns of the tables, kTableThreads apart) and walks over a share of
+// the pairs; 32 neighbouring threads write one 128-byte line of each table.  Tokens m, m + P, m + 2P, ... have the
+// same position and get the same values.  Bound by its stores, 8 bytes per (token, pair), if the instructions are
+// few: 131075 tokens, 64 pairs (floor 10.6 us): 27 us with a 64-bit reduction and the library's sine and cosine,
+// 18.9 us with fixed-point turns and one token per thread (20 of 55 instructions were the loop's).
+constexpr int kTokens = 4;
 struct TableParams {
   const void* pos;
   int axes, P, M, pairs, rot_pairs;
@@ -414,41 +420,59 @@ __global__ void __launch_bounds__(kTableThreads)
 rope_tables_kernel(const __grid_constant__ TableParams p, const __grid_constant__ Freqs fr) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const int m0 = blockIdx.x * kTableThreads + threadIdx.x;
-  if (m0 >= p.P) return;
+  const long long m0 = static_cast<long long>(blockIdx.x) * (kTableThreads * kTokens) + threadIdx.x;
   const int i0 = blockIdx.y * p.per, i1 = min(i0 + p.per, p.pairs);
   float* cos = p.cos + static_cast<long long>(i0) * p.M + m0;
   float* sin = p.sin + static_cast<long long>(i0) * p.M + m0;
-  int i = i0;
-  while (i < min(i1, p.rot_pairs)) {               // axis by axis
-    const int a = fr.axis[i];
-    float bad;
-    const uint32_t x = position<kFloat>(p.pos, static_cast<long long>(m0) * p.axes + a, bad);
-    int end = i + 1;
-    while (end < min(i1, p.rot_pairs) && fr.axis[end] == a) ++end;
-#pragma unroll 4
-    for (; i < end; ++i) {
-      float s, c;
-      sincos_turns(turn_fraction<kFloat>(x, fr.f[i]), s, c);
-      if (kFloat) {
-        s += bad;
-        c += bad;
-      }
-      cos[0] = c;
-      sin[0] = s;
-      for (long long m = p.P; m < p.M - m0; m += p.P) {
-        cos[m] = c;
-        sin[m] = s;
-      }
-      cos += p.M;
-      sin += p.M;
-    }
+  Position<kFloat> x[kTokens];
+  float bad[kTokens];
+  bool on[kTokens];
+#pragma unroll
+  for (int t = 0; t < kTokens; ++t) {
+    on[t] = m0 + t * kTableThreads < p.P;
+    x[t] = 0;
+    bad[t] = 0.f;
   }
-  for (; i < i1; ++i, cos += p.M, sin += p.M)      // pairs past the rotated columns stay as they are
-    for (long long m = 0; m < p.M - m0; m += p.P) {
-      cos[m] = 1.f;
-      sin[m] = 0.f;
+  const int more = p.M / p.P - 1;                  // further tokens with the same position
+  auto walk = [&](auto whole) {                    // whole: every token of the block, no further ones
+    auto put = [&](int t, float s, float c) {
+      if (!decltype(whole)::value && !on[t]) return;
+      cos[t * kTableThreads] = c;
+      sin[t * kTableThreads] = s;
+      if (!decltype(whole)::value)
+        for (int r = 1; r <= more; ++r) {
+          cos[t * kTableThreads + static_cast<long long>(r) * p.P] = c;
+          sin[t * kTableThreads + static_cast<long long>(r) * p.P] = s;
+        }
+    };
+    int i = i0;
+    while (i < min(i1, p.rot_pairs)) {             // axis by axis
+      const int a = fr.axis[i];
+#pragma unroll
+      for (int t = 0; t < kTokens; ++t)
+        if (on[t]) x[t] = position<kFloat>(p.pos, (m0 + t * kTableThreads) * p.axes + a, bad[t]);
+      do {
+        const uint64_t f = fr.f[i];
+#pragma unroll
+        for (int t = 0; t < kTokens; ++t) {
+          float s, c;
+          sincos_turns(turn_fraction(x[t], f), bad[t], s, c);
+          put(t, s, c);
+        }
+        cos += p.M;
+        sin += p.M;
+        ++i;
+      } while (i < min(i1, p.rot_pairs) && fr.axis[i] == a);
     }
+    for (; i < i1; ++i, cos += p.M, sin += p.M) {  // pairs past the rotated columns stay as they are
+#pragma unroll
+      for (int t = 0; t < kTokens; ++t) put(t, 0.f, 1.f);
+    }
+  };
+  if (more == 0 && (static_cast<long long>(blockIdx.x) + 1) * (kTableThreads * kTokens) <= p.P)
+    walk(std::true_type{});
+  else
+    walk(std::false_type{});
 }
 
 }  // namespace k9
