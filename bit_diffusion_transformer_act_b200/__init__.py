@@ -41,4 +41,4 @@ from .ops import (  # noqa: F401
     SvdqW4A4Linear,
     AwqW4A16Linear,
 )
-from .torch_ops import AwqLinear, SvdqLinear, swap_linears  # noqa: F401,E402
+from .torch_ops import AwqLinear, LoraLinear, SvdqLinear, attach_adapters, set_lora_plan, swap_linears  # noqa: F401,E402

@@ -15,9 +15,15 @@ Operators (all tensors on one CUDA device):
       w_global_scale float, N int, rank int) -> Y bf16 [M,N]
   svdq::awq_w4a16_linear(X bf16 [M,K], qweight u8 [N,K/2], scales bf16 [N,K/64],
       zeros bf16 [N,K/64], bias bf16 [N] or None) -> Y bf16 [M,N]
+  svdq::lora_add_(X bf16 [M,K], Y bf16 [M,N], A bf16 [adapters,rank,K], B bf16 [adapters,N,rank],
+      plan u8, plan_sizes int[9]) -> (), adds each request's adapters to Y
+  svdq::qk_norm_rope(q bf16 [M,Hq,D], k bf16 [M,Hk,D], norm_wq, norm_wk bf16 [D] or None, eps float,
+      positions int32 or fp32 [P,axes], axes_dims int[], theta float[], pairing str) -> (q', k')
+  svdq::rope_axes_tables(positions, axes_dims int[], theta float[], head_dim int, rows int)
+      -> (cos, sin fp32 [head_dim/2, rows])
 """
 
-from typing import Callable, Optional, Tuple
+from typing import Callable, List, Optional, Sequence, Tuple
 
 import numpy as np
 import torch
@@ -66,6 +72,41 @@ def awq_w4a16_linear(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tenso
 @awq_w4a16_linear.register_fake
 def _(X, qweight, scales, zeros, bias):
     return X.new_empty((X.shape[0], qweight.shape[0]), dtype=torch.bfloat16)
+
+
+@torch.library.custom_op("svdq::lora_add_", mutates_args={"Y"})
+def lora_add_(X: torch.Tensor, Y: torch.Tensor, A: torch.Tensor, B: torch.Tensor, plan: torch.Tensor,
+              plan_sizes: List[int]) -> None:
+    ops.svdq_lora_add(X, Y, A, B, ops.LoraPlan.from_parts(plan, plan_sizes), out=Y)
+
+
+@lora_add_.register_fake
+def _(X, Y, A, B, plan, plan_sizes):
+    return None
+
+
+@torch.library.custom_op("svdq::qk_norm_rope", mutates_args=())
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, norm_wq: Optional[torch.Tensor], norm_wk: Optional[torch.Tensor],
+                 eps: float, positions: torch.Tensor, axes_dims: List[int], theta: List[float],
+                 pairing: str) -> Tuple[torch.Tensor, torch.Tensor]:
+    return ops.svdq_qk_norm_rope(q, k, norm_wq, norm_wk, eps, positions, axes_dims, theta, pairing)
+
+
+@qk_norm_rope.register_fake
+def _(q, k, norm_wq, norm_wk, eps, positions, axes_dims, theta, pairing):
+    return q.new_empty(q.shape), k.new_empty(k.shape)
+
+
+@torch.library.custom_op("svdq::rope_axes_tables", mutates_args=())
+def rope_axes_tables(positions: torch.Tensor, axes_dims: List[int], theta: List[float], head_dim: int,
+                     rows: int) -> Tuple[torch.Tensor, torch.Tensor]:
+    return ops.svdq_rope_axes_tables(positions, axes_dims, theta, head_dim, rows)
+
+
+@rope_axes_tables.register_fake
+def _(positions, axes_dims, theta, head_dim, rows):
+    shape = (head_dim // 2, rows)
+    return positions.new_empty(shape, dtype=torch.float32), positions.new_empty(shape, dtype=torch.float32)
 
 
 # ---------------------------------------------------------------- layers
@@ -152,6 +193,82 @@ class AwqLinear(nn.Module):
 
     def extra_repr(self) -> str:
         return f"in_features={self.in_features}, out_features={self.out_features}, int4 group 64"
+
+
+class LoraLinear(nn.Module):
+    """A shared projection (an SvdqLinear, an AwqLinear, an nn.Linear) with a pool of low-rank adapters beside
+    it, of which each request of a batch uses its own: y = base(x) + sum_j w_j B_j (A_j x).
+
+    A bf16 [adapters, rank, in_features], B bf16 [adapters, out_features, rank].  Which rows use which adapters is
+    the batch's plan (``set_plan``; rows are counted after flattening the leading dimensions); without a plan
+    the layer is its base.  For inference: no gradients."""
+
+    def __init__(self, base: nn.Module, A: torch.Tensor, B: torch.Tensor):
+        super().__init__()
+        adapters, rank, k = A.shape
+        if k != base.in_features or tuple(B.shape) != (adapters, base.out_features, rank):
+            raise ValueError(f"A {tuple(A.shape)} and B {tuple(B.shape)} do not fit a projection from "
+                             f"{base.in_features} to {base.out_features}")
+        self.base = base
+        self.in_features, self.out_features = base.in_features, base.out_features
+        self.register_buffer("A", A)
+        self.register_buffer("B", B)
+        self.plan_words: Optional[torch.Tensor] = None
+        self.plan_sizes: List[int] = []
+
+    @classmethod
+    def from_adapters(cls, base: nn.Module, adapters: Sequence[Tuple[torch.Tensor, torch.Tensor]]) -> "LoraLinear":
+        """adapters: (A [r, in_features], B [out_features, r]) of any ranks r, padded here with zeros to the
+        largest, rounded up to a multiple of 16."""
+        rank = (max(a.shape[0] for a, _ in adapters) + 15) // 16 * 16
+        dev = adapters[0][0].device
+        A = torch.zeros((len(adapters), rank, base.in_features), dtype=torch.bfloat16, device=dev)
+        B = torch.zeros((len(adapters), base.out_features, rank), dtype=torch.bfloat16, device=dev)
+        for i, (a, b) in enumerate(adapters):
+            if a.shape[0] != b.shape[1]:
+                raise ValueError(f"adapter {i}: A has rank {a.shape[0]}, B {b.shape[1]}")
+            A[i, : a.shape[0]] = a
+            B[i, :, : b.shape[1]] = b
+        return cls(base, A, B)
+
+    def set_plan(self, plan: Optional[ops.LoraPlan]) -> None:
+        self.plan_words = None if plan is None else plan.words
+        self.plan_sizes = [] if plan is None else plan.sizes()
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        y = self.base(x)
+        if self.plan_words is None:
+            return y
+        y2 = y.reshape(-1, self.out_features)
+        torch.ops.svdq.lora_add_(_as_2d(x, self.in_features), y2, self.A, self.B, self.plan_words, self.plan_sizes)
+        return y2.reshape(y.shape)
+
+    def extra_repr(self) -> str:
+        return f"adapters={self.A.shape[0]}, rank={self.A.shape[1]}"
+
+
+def attach_adapters(model: nn.Module, factory: Callable[[str, nn.Module], Optional[nn.Module]]) -> int:
+    """Replaces, in place, every SvdqLinear, AwqLinear and nn.Linear of ``model`` for which
+    ``factory(qualified_name, layer)`` returns a module (for instance a LoraLinear around it); returns how
+    many were replaced."""
+    replaced = 0
+    for parent_name, parent in list(model.named_modules()):
+        if isinstance(parent, LoraLinear):
+            continue
+        for child_name, child in list(parent.named_children()):
+            if isinstance(child, (SvdqLinear, AwqLinear, nn.Linear)):
+                new = factory(f"{parent_name}.{child_name}" if parent_name else child_name, child)
+                if new is not None:
+                    setattr(parent, child_name, new)
+                    replaced += 1
+    return replaced
+
+
+def set_lora_plan(model: nn.Module, plan: Optional[ops.LoraPlan]) -> None:
+    """Sets the batch's plan (None: no adapters) on every LoraLinear of ``model``."""
+    for m in model.modules():
+        if isinstance(m, LoraLinear):
+            m.set_plan(plan)
 
 
 def swap_linears(model: nn.Module, factory: Callable[[str, nn.Linear], Optional[nn.Module]]) -> int:

@@ -1,0 +1,75 @@
+"""The adapter layers and the new torch.library operators on the host: registration, fake implementations,
+tracing, padding of the pool, and the swap."""
+
+import pytest
+import torch
+from torch import nn
+
+import bit_diffusion_transformer_act_b200 as P
+from bit_diffusion_transformer_act_b200 import torch_ops as T
+
+
+def _meta(*shape, dtype=torch.bfloat16):
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+def test_operators_registered():
+    for name in ("lora_add_", "qk_norm_rope", "rope_axes_tables"):
+        assert hasattr(torch.ops.svdq, name), name
+
+
+def test_fake_shapes():
+    q, k = torch.ops.svdq.qk_norm_rope(_meta(7, 4, 64), _meta(7, 2, 64), None, None, 0.0,
+                                       _meta(7, 2, dtype=torch.int32), [32, 32], [1e4, 1e4], "half")
+    assert q.shape == (7, 4, 64) and k.shape == (7, 2, 64)
+    cos, sin = torch.ops.svdq.rope_axes_tables(_meta(7, 2, dtype=torch.int32), [32, 32], [1e4, 1e4], 64, 14)
+    assert cos.shape == sin.shape == (32, 14) and cos.dtype == torch.float32
+
+
+def _awq(K=512, N=128):
+    return T.AwqLinear(torch.zeros((N, K // 2), dtype=torch.uint8), torch.zeros((N, K // 64), dtype=torch.bfloat16),
+                       torch.zeros((N, K // 64), dtype=torch.bfloat16))
+
+
+def _pool(K=512, N=128, ranks=(4, 16, 20)):
+    return [(torch.ones((r, K), dtype=torch.bfloat16), torch.full((N, r), 2.0, dtype=torch.bfloat16)) for r in ranks]
+
+
+def test_pool_is_padded_with_zero_ranks():
+    layer = T.LoraLinear.from_adapters(_awq(), _pool())
+    assert layer.A.shape == (3, 32, 512) and layer.B.shape == (3, 128, 32)
+    assert (layer.A[0, :4] == 1).all() and (layer.A[0, 4:] == 0).all() and (layer.B[2, :, 20:] == 0).all()
+    with pytest.raises(ValueError, match="rank"):
+        T.LoraLinear.from_adapters(_awq(), [(torch.ones(4, 512), torch.ones(128, 5))])
+    with pytest.raises(ValueError, match="do not fit"):
+        T.LoraLinear(_awq(), torch.zeros(3, 16, 512), torch.zeros(3, 64, 16))
+
+
+def test_attach_set_and_trace():
+    model = nn.Sequential(_awq(), nn.GELU(), nn.Sequential(nn.Linear(128, 128), nn.Linear(128, 64)))
+    seen = []
+
+    def factory(name, layer):
+        seen.append(name)
+        return T.LoraLinear.from_adapters(layer, _pool()) if isinstance(layer, T.AwqLinear) else None
+
+    assert T.attach_adapters(model, factory) == 1
+    assert seen == ["0", "2.0", "2.1"] and isinstance(model[0], T.LoraLinear)
+    assert T.attach_adapters(model, lambda name, layer: None) == 0
+    plan = P.LoraPlan([0, 2, 6], [1, -1], [1.0, 1.0], 6, 3, device="cpu")
+    x = torch.zeros((2, 3, 512), dtype=torch.bfloat16)
+
+    def calls(m):
+        return [str(n.target) for n in torch.export.export(m, (x,)).graph.nodes if n.op == "call_function"]
+
+    assert not any("lora" in c for c in calls(model[0]))
+    T.set_lora_plan(model, plan)
+    assert any("svdq.lora_add_" in c or "auto_functionalized" in c for c in calls(model[0]))
+    T.set_lora_plan(model, None)
+    assert not any("lora" in c for c in calls(model[0]))
+
+
+def test_state_dict_carries_the_pool():
+    a, b = T.LoraLinear.from_adapters(_awq(), _pool()), T.LoraLinear.from_adapters(_awq(), _pool(ranks=(1, 1, 32)))
+    b.load_state_dict(a.state_dict())
+    assert torch.equal(a.A, b.A) and torch.equal(a.B, b.B)
