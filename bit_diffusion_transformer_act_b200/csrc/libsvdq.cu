@@ -1037,12 +1037,19 @@ static int lora_groups_launch(const LoraCall& c, bool copy, float* part) {
       return SVDQ_ERR_CUDA;
   }
   const int all = p.ngroups + (copy ? c.plan->copy_groups : 0);
-  const int strips = (c.N / 16 + k11::kWarps - 1) / k11::kWarps;
-  const dim3 grid(all, std::max(1, std::min(strips, 4 * sm_count(c.dev) / all)));
-#define SVDQ_LORA_UP(WIDE_, STEPS_)                                                                              \
-  case STEPS_:                                                                                                   \
-    return launch_pdl(k11::lora_short_up_kernel<WIDE_, STEPS_>, grid, k11::kThreads, 0, 1, c.stream, p) ? SVDQ_OK \
-                                                                                                         : SVDQ_ERR_CUDA
+  const int strips = (c.N / k11::kUpCols + k11::kUpWarps - 1) / k11::kUpWarps;
+  const dim3 grid(all, std::max(1, std::min(strips, 4 * sm_count(c.dev) / all)));   // four CTAs per SM
+  const int passes = (strips - 1) / static_cast<int>(grid.y) + 1;
+  const int piece = k11::kUpWarps * k11::up_piece_bytes(c.jr);   // of all warps of a CTA
+  p.depth = std::max(2, std::min({k11::kUpMaxDepth, k11::kUpRingBytes / piece, passes}));
+  const int smem = p.depth * piece;
+#define SVDQ_LORA_UP(WIDE_, STEPS_)                                                                                  \
+  case STEPS_:                                                                                                       \
+    return set_smem_once<k11::lora_short_up_kernel<WIDE_, STEPS_>>(                                                  \
+               std::max(k11::kUpRingBytes, 2 * k11::kUpWarps * k11::up_piece_bytes(svdq::kLoraMaxRank)), c.dev) &&  \
+                   launch_pdl(k11::lora_short_up_kernel<WIDE_, STEPS_>, grid, k11::kUpThreads, smem, 1, c.stream, p) \
+               ? SVDQ_OK                                                                                             \
+               : SVDQ_ERR_CUDA
   if (c.rank % 32 == 0) {
     switch (c.jr / 32) {
       SVDQ_LORA_UP(true, 1);
@@ -1107,10 +1114,25 @@ int svdq_lora_add(const void* X, int64_t ldx, const void* Yin, int64_t ldyin, co
   return launch_status();
 }
 
-// The pairs' frequencies in turns per unit of position, as the kernels read them (see Freqs); returns the
-// rotated width.  Along an axis they are a geometric sequence, formed in extended precision (128 products
-// of 2^-64 each).
-static int rope_freqs(int axes, const int32_t* dims, const double* theta, bool is_float, svdq::k9::Freqs* fr) {
+// The pairs' frequencies in turns per unit of position, as the kernels read them (see Freqs).  Along an axis they
+// are a geometric sequence, formed in extended precision (128 products of 2^-64 each).  They follow from the
+// axes alone, and a model has one set: the last one of the thread is kept with what it was formed from
+// (forming it costs as much as a launch).
+struct RopeFreqs {
+  int axes = 0, is_float = 0, rot = 0;
+  int32_t dims[svdq::k9::kMaxAxes];
+  double theta[svdq::k9::kMaxAxes];
+  svdq::k9::Freqs fr;
+};
+static const RopeFreqs& rope_freqs(int axes, const int32_t* dims, const double* theta, bool is_float) {
+  static thread_local RopeFreqs r;
+  if (r.axes == axes && r.is_float == is_float && memcmp(r.dims, dims, axes * sizeof(int32_t)) == 0 &&
+      memcmp(r.theta, theta, axes * sizeof(double)) == 0)
+    return r;
+  r.axes = axes;
+  r.is_float = is_float;
+  memcpy(r.dims, dims, axes * sizeof(int32_t));
+  memcpy(r.theta, theta, axes * sizeof(double));
   int at = 0;
   for (int a = 0; a < axes; ++a) {
     const long double ratio = std::pow(static_cast<long double>(theta[a]), -2.0L / dims[a]);
@@ -1118,20 +1140,20 @@ static int rope_freqs(int axes, const int32_t* dims, const double* theta, bool i
     for (int i = 0; i < dims[a] / 2; ++i, ++at) {
       if (is_float) {
         const double d = static_cast<double>(f);
-        memcpy(&fr->f[at], &d, sizeof(d));
+        memcpy(&r.fr.f[at], &d, sizeof(d));
       } else {
-        fr->f[at] = static_cast<uint64_t>(std::ldexp(f - std::floor(f), 64));   // whole turns do not count
+        r.fr.f[at] = static_cast<uint64_t>(std::ldexp(f - std::floor(f), 64));   // whole turns do not count
       }
-      fr->axis[at] = static_cast<uint8_t>(a);
+      r.fr.axis[at] = static_cast<uint8_t>(a);
       f *= ratio;
     }
   }
-  const int rot = 2 * at;
+  r.rot = 2 * at;
   for (; at < svdq::k9::kMaxPairs; ++at) {
-    fr->f[at] = 0;
-    fr->axis[at] = 0;
+    r.fr.f[at] = 0;
+    r.fr.axis[at] = 0;
   }
-  return rot;
+  return r;
 }
 
 // Checks of the arguments that both rotary calls share.
@@ -1210,9 +1232,10 @@ int svdq_qk_norm_rope(const void* Q, int64_t q_row_stride, int64_t q_head_stride
   if (int st = current_device_ok(&dev)) return st;
 
   namespace k9 = svdq::k9;
-  k9::Freqs fr;
+  const RopeFreqs& rf = rope_freqs(axes, axis_dims, axis_theta, positions_float != 0);
+  const k9::Freqs& fr = rf.fr;
   k9::Params p;
-  p.rot = rope_freqs(axes, axis_dims, axis_theta, positions_float != 0, &fr);
+  p.rot = rf.rot;
   auto view = [](const HeadsView& v) {
     return k9::View{static_cast<__nv_bfloat16*>(const_cast<void*>(v.ptr)), v.row, v.head};
   };
@@ -1291,15 +1314,15 @@ int svdq_rope_axes_tables(const void* positions, int positions_float, int P, int
   int dev;
   if (int st = current_device_ok(&dev)) return st;
   namespace k9 = svdq::k9;
-  k9::Freqs fr;
+  const RopeFreqs& rf = rope_freqs(axes, axis_dims, axis_theta, positions_float != 0);
+  const k9::Freqs& fr = rf.fr;
   k9::TableParams p;
-  const int rot = rope_freqs(axes, axis_dims, axis_theta, positions_float != 0, &fr);
   p.pos = positions;
   p.axes = axes;
   p.P = P;
   p.M = M;
   p.pairs = head_dim / 2;
-  p.rot_pairs = rot / 2;
+  p.rot_pairs = rf.rot / 2;
   p.cos = static_cast<float*>(rope_cos);
   p.sin = static_cast<float*>(rope_sin);
   const int bx = (P - 1) / (k9::kTableThreads * k9::kTokens) + 1;

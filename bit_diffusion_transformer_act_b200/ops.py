@@ -678,16 +678,37 @@ _PAIRINGS = {"interleaved": 0, "half": 1}
 def _heads(t, M, D, name, dev):
     """A bf16 [M, heads, D] tensor on device `dev` (the current one) with any strides over tokens and heads:
     (address, token stride, head stride, heads)."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[0] != M or \
-            t.shape[2] != D:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.dim() != 3:
         raise ValueError(f"{name}: expected a torch.bfloat16 tensor [{M}, heads, {D}], got "
                          f"{getattr(t, 'dtype', type(t))} {tuple(getattr(t, 'shape', ()))}")
+    rows, heads, width = t.shape
     row, head, inner = t.stride()
+    if rows != M or width != D:
+        raise ValueError(f"{name}: expected a torch.bfloat16 tensor [{M}, heads, {D}], got {tuple(t.shape)}")
     if inner != 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
     if not t.get_device() == dev >= 0:
         _on_device(t, name)
-    return t.data_ptr(), row, head, t.shape[1]
+    return t.data_ptr(), row, head, heads
+
+
+def _heads_in_out(t, out, w, M, D, name, dev):
+    """(address, token stride, head stride, heads) of q or k, its output and that one's address and strides, the
+    address of its norm weights; a missing t has none of them."""
+    if t is None:
+        if out is not None or w is not None:
+            raise ValueError(f"out_{name} and norm_w{name} need {name}")
+        return None, 0, 0, 0, None, None, 0, 0, None
+    tp, row, head, heads = _heads(t, M, D, name, dev)
+    if out is None:
+        out = t.new_empty((M, heads, D))
+        op, orow, ohead = out.data_ptr(), heads * D, D
+    else:
+        op, orow, ohead, oheads = _heads(out, M, D, "out_" + name, dev)
+        if oheads != heads:
+            raise ValueError(f"out_{name} must have {heads} heads, got {oheads}")
+    wp = _addr(w, torch.bfloat16, (D,), "norm_w" + name, dev) if w is not None else None
+    return tp, row, head, heads, out, op, orow, ohead, wp
 
 
 def svdq_qk_norm_rope(q, k, norm_wq, norm_wk, eps, positions, axes_dims, theta, pairing="interleaved", out_q=None,
@@ -702,33 +723,14 @@ def svdq_qk_norm_rope(q, k, norm_wq, norm_wk, eps, positions, axes_dims, theta, 
     dev, P, axes, is_float, dims, thetas = _rope_axes(positions, axes_dims, theta)
     if pairing not in _PAIRINGS:
         raise ValueError(f"pairing: one of {sorted(_PAIRINGS)}, got {pairing!r}")
-    views = []
-    outs = []
-    for t, out, w, name in ((q, out_q, norm_wq, "q"), (k, out_k, norm_wk, "k")):
-        if t is None:
-            if out is not None or w is not None:
-                raise ValueError(f"out_{name} and norm_w{name} need {name}")
-            views.append((None, 0, 0, 0, None, 0, 0, None))
-            outs.append(None)
-            continue
-        tp, row, head, heads = _heads(t, M, D, name, dev)
-        if out is None:
-            out = t.new_empty((M, heads, D))
-            op, orow, ohead = out.data_ptr(), heads * D, D
-        else:
-            op, orow, ohead, oheads = _heads(out, M, D, "out_" + name, dev)
-            if oheads != heads:
-                raise ValueError(f"out_{name} must have {heads} heads, got {oheads}")
-        wp = _addr(w, torch.bfloat16, (D,), "norm_w" + name, dev) if w is not None else None
-        views.append((tp, row, head, heads, op, orow, ohead, wp))
-        outs.append(out)
-    (qp, qr, qh, nq, oqp, oqr, oqh, wq), (kp, kr, kh, nk, okp, okr, okh, wk) = views
+    qp, qr, qh, nq, out_q, oqp, oqr, oqh, wq = _heads_in_out(q, out_q, norm_wq, M, D, "q", dev)
+    kp, kr, kh, nk, out_k, okp, okr, okh, wk = _heads_in_out(k, out_k, norm_wk, M, D, "k", dev)
     st = LIB.svdq_qk_norm_rope(qp, qr, qh, nq, kp, kr, kh, nk, M, D, wq, wk, eps, positions.data_ptr(), is_float, P,
                                axes, dims, thetas, _PAIRINGS[pairing], oqp, oqr, oqh, okp, okr, okh,
                                torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _check("svdq_qk_norm_rope", st)
-    return tuple(outs)
+    return out_q, out_k
 
 
 def svdq_rope_axes_tables(positions, axes_dims, theta, head_dim, rows=None, rope_cos=None, rope_sin=None):
