@@ -1170,7 +1170,7 @@ static int rope_check(const void* positions, int P, int axes, const int32_t* dim
   if (rot % 8 != 0 || rot > head_dim) return SVDQ_ERR_UNSUPPORTED_SHAPE;
   if (M == 0) return SVDQ_OK;
   if (P <= 0 || M % P != 0) return SVDQ_ERR_INVALID_ARG;
-  if (!positions || !aligned16(positions)) return SVDQ_ERR_INVALID_ARG;
+  if (!positions || (reinterpret_cast<uintptr_t>(positions) & 3u)) return SVDQ_ERR_INVALID_ARG;
   return SVDQ_OK;
 }
 

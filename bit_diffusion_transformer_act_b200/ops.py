@@ -595,7 +595,7 @@ def _row_strided(t, rows, cols, name, dev):
                          f"{getattr(t, 'dtype', type(t))} {tuple(getattr(t, 'shape', ()))}")
     ld, inner = t.stride()
     if rows <= 1:
-        ld = max(cols, ld)
+        ld = cols
     if (cols > 1 and inner != 1) or ld < cols:
         raise ValueError(f"{name}: rows must be contiguous and must not overlap")
     if not t.get_device() == dev >= 0:
@@ -719,6 +719,8 @@ def svdq_qk_norm_rope(q, k, norm_wq, norm_wk, eps, positions, axes_dims, theta, 
     (token m has position m % P), axes_dims the rotated columns of each axis, theta one value or one per axis,
     pairing "interleaved" or "half".  out_q / out_k: q / k themselves for in place, tensors of their
     shape, or None for new ones.  Returns (out_q, out_k)."""
+    if q is None and k is None:
+        raise ValueError("q or k is needed")
     M, _, D = (q if q is not None else k).shape
     dev, P, axes, is_float, dims, thetas = _rope_axes(positions, axes_dims, theta)
     if pairing not in _PAIRINGS:

@@ -397,11 +397,12 @@ int svdq_lora_add(const void* X, int64_t ldx, const void* Yin, int64_t ldyin, co
  *   norm_wq, norm_wk  device bf16 [head_dim], or NULL: no normalisation of q or k (eps is then not used)
  *   pairing 0: pair i is (x[2 i], x[2 i + 1]) (as svdq_w4a4_nvfp4_linear_qkv); 1: (x[i], x[i + rotated / 2])
  *   out_q may be Q with Q's strides (in place), likewise out_k; an output overlaps nothing else.
- * head_dim % 8 == 0, 8..256; every pointer 16-byte aligned.
+ * head_dim % 8 == 0, 8..256; Q, K, the outputs and the norm weights 16-byte aligned, positions 4-byte aligned;
+ * q_heads, k_heads <= 65536, and M times the heads below 2^31.
  *
  * svdq_rope_axes_tables (kernel 10): the cos / sin tables of the same positions in the layout that
  * svdq_w4a4_nvfp4_linear_qkv reads: float32 [head_dim / 2, M], pair-major; pairs past the rotated width
- * get 1 and 0.  head_dim even, 2..256.
+ * get 1 and 0.  head_dim even, 2..256; the tables 16-byte aligned.
  * Errors and asynchrony as svdq_w4a4_nvfp4_linear. */
 int svdq_qk_norm_rope(const void* Q, int64_t q_row_stride, int64_t q_head_stride, int q_heads, const void* K,
                       int64_t k_row_stride, int64_t k_head_stride, int k_heads, int M, int head_dim,

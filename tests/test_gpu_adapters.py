@@ -191,3 +191,72 @@ def test_two_streams_at_once(P):
     for i, (x, y, a, b, off, ids, w, plan, _) in enumerate(sets):
         _check(outs[i][0], x, y, a, b, off, ids, w)
         assert all(torch.equal(o, outs[i][0]) for o in outs[i])
+
+
+def test_the_next_requests_nan_rows_do_not_reach_a_partial_tile(P):
+    """A tile of 78 rows is loaded in slabs of 32: the rows behind it belong to the next request."""
+    M, K, N = 300, 256, 192
+    x, y, a, b = _make(M, K, N, 32, 1, 2)
+    off, ids = [0, 78, 156, 300], np.array([[0], [1], [0]])
+    w = _weights(ids)
+    plan = P.LoraPlan(off, ids, w, M, 2)
+    expect = P.svdq_lora_add(x, y, a, b, plan)
+    x[78:156] = float("nan")
+    y[156:] = float("inf")
+    got = P.svdq_lora_add(x, y, a, b, plan)
+    assert torch.equal(got[:78], expect[:78])
+    assert torch.isnan(got[78:156].float()).all() and torch.isinf(got[156:].float()).all()
+
+
+@pytest.mark.parametrize("off", [[0, 4200], [0, 4000, 4001, 4017, 4200], list(range(0, 4201, 10))])
+def test_offsets_past_32_bits(P, off):
+    """Rows 2^20 elements apart: the last ones start beyond 2^32 elements (and 2^33 bytes)."""
+    M, K, N, ld = 4200, 64, 128, 1 << 20
+    x, y, a, b = _make(M, K, N, 16, 1, 3)
+    wide = torch.empty((M, ld), dtype=torch.bfloat16, device="cuda")
+    wide[:, 512:512 + N] = y
+    wide[:, 512 + N:1024] = 3.0
+    ids = np.arange(len(off) - 1)[:, None] % 3
+    w = _weights(ids)
+    plan = P.LoraPlan(off, ids, w, M, 3)
+    win = wide[:, 512:512 + N]
+    P.svdq_lora_add(x, win, a, b, plan, out=win)
+    assert torch.equal(win, P.svdq_lora_add(x, y, a, b, plan))
+    assert (wide[:, 512 + N:1024] == 3).all()
+
+
+def test_many_adapters_in_one_batch(P):
+    """More requests than a wave has CTAs, each row its own adapter; and long requests of one row more than a
+    tile."""
+    M, K, N = 700, 64, 64
+    x, y, a, b = _make(M, K, N, 16, 1, 700)
+    off, ids = list(range(M + 1)), np.arange(M)[:, None]
+    w = _weights(ids)
+    _check(P.svdq_lora_add(x, y, a, b, P.LoraPlan(off, ids, w, M, M)), x, y, a, b, off, ids, w)
+    off, ids = [0, 129, 258, 387, 516, 645], np.array([[5], [5], [699], [-1], [0]])
+    w = _weights(ids)
+    _check(P.svdq_lora_add(x, y, a, b, P.LoraPlan(off, ids, w, M, M)), x, y, a, b, off, ids, w)
+
+
+def test_the_output_carries_no_autograd_graph(P):
+    """The calls are for inference, as the layers' are: their results are no part of a graph."""
+    x, y, a, b = _make(20, 64, 64, 16, 1, 1)
+    plan = P.LoraPlan([0, 20], [0], [1.0], 20, 1)
+    out = P.svdq_lora_add(x.requires_grad_(), y, a, b, plan)
+    assert not out.requires_grad
+
+
+def test_device_and_stream(P):
+    """On a side stream, ordered by events with the tensors' own; a plan on the host is refused."""
+    x, y, a, b = _make(200, 512, 256, 32, 1, 2)
+    off, ids = [0, 5, 200], np.array([[0], [1]])
+    w = _weights(ids)
+    plan = P.LoraPlan(off, ids, w, 200, 2)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out = P.svdq_lora_add(x, y, a, b, plan)
+    torch.cuda.current_stream().wait_stream(side)
+    _check(out, x, y, a, b, off, ids, w)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        P.svdq_lora_add(x, y, a, b, P.LoraPlan(off, ids, w, 200, 2, device="cpu"))

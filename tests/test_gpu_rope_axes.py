@@ -129,3 +129,77 @@ def test_far_positions_keep_their_angle(P):
     ang = oracle.angles(_np(pos), [64], [10000.0]).T
     tol = 2.0 ** -22 + np.abs(ang) * 2.0 ** -45
     assert (np.abs(_np(cos) - np.cos(ang)) <= tol).all() and (np.abs(_np(sin) - np.sin(ang)) <= tol).all()
+
+
+def test_offsets_past_32_bits(P):
+    """Tokens 2^20 elements apart: the last ones start beyond 2^32 elements."""
+    M, H, D, ld = 4200, 3, 64, 1 << 20
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q = torch.randn((M, H, D), generator=g, device="cuda").to(torch.bfloat16)
+    wide = torch.empty((M, ld), dtype=torch.bfloat16, device="cuda")
+    wide[:, 512:512 + H * D] = q.view(M, H * D)
+    wide[:, 512 + H * D:1024] = 3.0
+    win = wide[:, 512:512 + H * D].unflatten(1, (H, D))
+    w = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    pos = _positions(M, 2, False, 1)
+    expect, _ = P.svdq_qk_norm_rope(q, None, w, None, 1e-6, pos, [32, 32], 1e4)
+    P.svdq_qk_norm_rope(win, None, w, None, 1e-6, pos, [32, 32], 1e4, out_q=win)
+    assert torch.equal(win, expect) and (wide[:, 512 + H * D:1024] == 3).all()
+
+
+def test_a_slice_of_positions_and_every_token_alone(P):
+    """Positions that start anywhere in a longer list; one token at a time gives the same bits."""
+    q = torch.randn((40, 20, 128), device="cuda").to(torch.bfloat16)
+    k = torch.randn((40, 4, 128), device="cuda").to(torch.bfloat16)
+    w = torch.randn(128, device="cuda").to(torch.bfloat16)
+    for fractional in (False, True):
+        pos = _positions(43, 3, fractional, 3)
+        a = P.svdq_qk_norm_rope(q, k, w, w, 1e-5, pos[3:], [16, 56, 56], 1e4)
+        for m in (0, 1, 17, 39):
+            b = P.svdq_qk_norm_rope(q[m:m + 1], k[m:m + 1], w, w, 1e-5, pos[3 + m:4 + m], [16, 56, 56], 1e4)
+            assert torch.equal(a[0][m:m + 1], b[0]) and torch.equal(a[1][m:m + 1], b[1])
+
+
+def test_many_heads_and_units(P):
+    """More heads than a stage holds, few and many tokens, uneven q and k."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    w = torch.randn(128, generator=g, device="cuda").to(torch.bfloat16)
+    for M, hq, hk in ((1, 130, 1), (5, 64, 8), (600, 70, 3), (2400, 24, 24), (5000, 1, 9)):
+        q = torch.randn((M, hq, 128), generator=g, device="cuda").to(torch.bfloat16)
+        k = torch.randn((M, hk, 128), generator=g, device="cuda").to(torch.bfloat16)
+        pos = _positions(M, 3, False, M)
+        oq, ok = P.svdq_qk_norm_rope(q, k, w, None, 1e-6, pos, [44, 42, 42], 1e4)
+        pick = sorted({0, M // 2, M - 1})
+        for out, x, nw in ((oq, q, w), (ok, k, None)):
+            _check(out[pick], x[pick], nw, 1e-6, pos[pick], [44, 42, 42], [1e4] * 3, False, len(pick))
+        # all tokens against the halves' kernel on columns sorted even before odd (its sums differ in order)
+        order = torch.cat([torch.arange(0, 128, 2), torch.arange(1, 128, 2)]).cuda()
+        hq_, _ = P.svdq_qk_norm_rope(q[..., order].contiguous(), None, w[order].contiguous(), None, 1e-6, pos, [44, 42, 42],
+                                     1e4, "half")
+        d = (hq_.float() - oq[..., order].float()).abs()
+        assert (d <= 2.0 ** -7 * oq[..., order].float().abs() + 2.0 ** -14).all()
+
+
+def test_nan_positions_and_nothing_else(P):
+    q = torch.randn((3, 2, 16), device="cuda").to(torch.bfloat16)
+    pos = torch.tensor([[1.0], [float("nan")], [float("inf")]], device="cuda")
+    out, _ = P.svdq_qk_norm_rope(q, None, None, None, 0.0, pos, [8], 100.0)
+    assert torch.isfinite(out[0].float()).all()
+    assert torch.isnan(out[1:, :, :8].float()).all() and torch.equal(out[1:, :, 8:], q[1:, :, 8:])
+    cos, sin = P.svdq_rope_axes_tables(pos, [8], 100.0, 16)
+    assert torch.isnan(cos[:4, 1:]).all() and torch.isnan(sin[:4, 1:]).all() and (cos[4:] == 1).all()
+
+
+def test_a_graph_reads_new_positions(P):
+    q = torch.randn((300, 4, 64), device="cuda").to(torch.bfloat16)
+    pos, other = _positions(300, 2, False, 1), _positions(300, 2, False, 2)
+    P.svdq_qk_norm_rope(q, None, None, None, 0.0, pos, [32, 32], 1e4)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, _ = P.svdq_qk_norm_rope(q, None, None, None, 0.0, pos, [32, 32], 1e4)
+        cos, _ = P.svdq_rope_axes_tables(pos, [32, 32], 1e4, 64)
+    pos.copy_(other)
+    graph.replay()
+    assert torch.equal(out, P.svdq_qk_norm_rope(q, None, None, None, 0.0, other, [32, 32], 1e4)[0])
+    assert torch.equal(cos, P.svdq_rope_axes_tables(other, [32, 32], 1e4, 64)[0])
+    assert P.svdq_device_status() == 0

@@ -52,6 +52,8 @@ def test_valid_calls_reach_the_device():
     # into the thirds of another packed buffer
     assert _rope(oq=_at(70), oqs=(768, 128), ok=_at(70, 512), oks=(768, 128)) == OK
     assert _tables() == OK
+    assert _tables(pos=_at(1, 4)) == OK                 # a slice of a longer list of positions
+    assert _rope(pos=_at(66, 12)) == OK
 
 
 def test_empty_calls():
@@ -76,7 +78,7 @@ def test_refusals_of_both():
         assert call(P_=3) == 1
         assert call(P_=0) == 1
         assert call(pos=None) == 1
-        assert call(pos=_at(1, 4)) == 1
+        assert call(pos=_at(1, 2)) == 1
     assert _tables(cos=None) == 1
     assert _tables(sin=_at(1, 8)) == 1
     assert _tables(D=127, dims=(16, 56, 48)) == 2
@@ -112,6 +114,8 @@ def test_python_wrappers_refuse_before_the_call():
         P.svdq_qk_norm_rope(q, None, None, None, 0.0, pos, [16, 56, 56], 10000.0)
     with pytest.raises(ValueError, match="int32 or float32"):
         P.svdq_rope_axes_tables(pos.long(), [16, 56, 56], 10000.0, 128)
+    with pytest.raises(ValueError, match="q or k"):
+        P.svdq_qk_norm_rope(None, None, None, None, 0.0, pos, [16, 56, 56], 10000.0)
     with pytest.raises(ValueError, match="int32 or float32"):
         P.svdq_rope_axes_tables(pos[:, :2], [16, 56], 10000.0, 128)
 
