@@ -380,7 +380,8 @@ lora_tile_up_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
     }
   } else if (warp >= kUWarp0) {
     // ---------------------------------------------------------------- U: a row per thread, two warps per lane
-    // quarter taking blocks of 16 ranks in turn
+    // quarter taking blocks of 16 ranks in turn.  (With the epilogue's warps helping at a CTA's first tile, which
+    // everything waits for, 64 and 128 ranks stayed within 1 % and 32 ranks lost 1.5 us of 30 to spilled registers.)
     if (p.early) grid_dependency_wait();            // kernel 13 is done
     const int q = warp & 3;
     const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(kTmemU);
@@ -388,6 +389,8 @@ lora_tile_up_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
     int nu = 0;
     for (int t = i0 / p.chunks; t < p.ntiles && t * static_cast<long long>(p.chunks) < i1; ++t, ++nu) {
       const int32_t* rec = p.tiles + static_cast<size_t>(t) * tile_words + 4;
+      const int my_id = lane < p.slots ? __ldcg(rec + lane) : -1;   // lane j: slot j's adapter and weight
+      const float my_w = lane < p.slots ? __int_as_float(__ldcg(rec + p.slots + lane)) : 0.f;
       const float4* src = reinterpret_cast<const float4*>(p.parts) + t * p.ks * part + q * 32 + lane;
       if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(u_empty(nu & 1), ((nu >> 1) & 1u) ^ 1u, abort_flag, 82))) break;
       tc_fence_after();
@@ -396,7 +399,7 @@ lora_tile_up_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
         float4 u[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) u[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int z = 0; z < p.ks; z += 4) {         // 16 loads in flight; added in slice order
+        for (int z = 0; z < p.ks; z += 4) {           // 16 loads in flight; added in slice order
           float4 v[4][4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -415,8 +418,8 @@ lora_tile_up_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
               }
         }
         const int slot = c / p.rank;
-        const bool has = __ldcg(rec + slot) >= 0;   // an empty slot adds nothing, whatever is in X
-        const float w = __int_as_float(__ldcg(rec + p.slots + slot));
+        const bool has = __shfl_sync(0xFFFFFFFFu, my_id, slot) >= 0;   // an empty slot adds nothing, whatever is in X
+        const float w = __shfl_sync(0xFFFFFFFFu, my_w, slot);
         uint32_t hi[8], lo[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
