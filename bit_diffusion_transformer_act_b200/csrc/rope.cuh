@@ -134,7 +134,8 @@ __device__ __forceinline__ void store_v(__nv_bfloat16* p, const uint32_t (&r)[V 
 // Bound by memory (q and k read and written once: 4 bytes a value) if the instructions are few and enough
 // bytes are on their way.  9216 tokens of 40 heads of 128 (floor 29 us): 61 us with the sines formed by every
 // lane, the weights unpacked per head and scalar arithmetic (2940 warp instructions per token); 43 us without
-// that, the next heads of a warp prefetched into registers (16 KB per SM on their way).
+// that, the next heads of a warp prefetched into registers (16 KB per SM on their way); 37 us as it is (the
+// copies alone, without the arithmetic, 35.5).
 template <int V, int LPR, bool kHalf, bool kFloat>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 qk_norm_rope_kernel(const __grid_constant__ Params p, const __grid_constant__ Freqs fr) {
@@ -406,7 +407,7 @@ qk_norm_rope_kernel(const __grid_constant__ Params p, const __grid_constant__ Fr
 // the pairs; 32 neighbouring threads write one 128-byte line of each table.  Tokens m, m + P, m + 2P, ... have the
 // same position and get the same values.  Bound by its stores, 8 bytes per (token, pair), if the instructions are
 // few: 131075 tokens, 64 pairs (floor 10.6 us): 27 us with a 64-bit reduction and the library's sine and cosine,
-// 18.9 us with fixed-point turns and one token per thread (20 of 55 instructions were the loop's).
+// 18.9 us with fixed-point turns and one token per thread (20 of 55 instructions were the loop's), 15.2 us with four.
 constexpr int kTokens = 4;
 struct TableParams {
   const void* pos;
