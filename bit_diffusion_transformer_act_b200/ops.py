@@ -8,6 +8,7 @@ is not sm_100 the calls raise.
 
 import ctypes
 import functools
+import operator
 import os
 
 import numpy as np
@@ -537,14 +538,15 @@ class LoraPlan:
 
     row_offsets [requests + 1] (host integers): request s owns rows row_offsets[s] .. row_offsets[s + 1] - 1
     of the `rows` rows; adapter_ids [requests, slots] (or [requests]), -1 for none; weights the same shape;
-    adapters: how many the pool holds.  The plan is uploaded on the current stream."""
+    adapters: how many the pool holds.  The plan is on the device when the constructor returns; keep it until the
+    calls that use it, on whatever stream, and the graphs that hold such calls are done."""
 
     def __init__(self, row_offsets, adapter_ids, weights, rows, adapters, device="cuda"):
         off = _int32_array(row_offsets, "row_offsets").reshape(-1)
         ids = _int32_array(adapter_ids, "adapter_ids")
         w = np.ascontiguousarray(weights, dtype=np.float32)
         if ids.ndim == 1:
-            ids, w = ids[:, None], w.reshape(ids.shape[0], -1)
+            ids, w = ids[:, None], w.reshape(-1, 1)
         if ids.ndim != 2 or ids.shape != w.shape or off.shape[0] != ids.shape[0] + 1:
             raise ValueError("row_offsets must be [requests + 1], adapter_ids and weights [requests, slots]")
         self.rows, self.adapters = int(rows), int(adapters)
@@ -668,7 +670,9 @@ def _rope_axes(positions, axes_dims, theta):
     P, axes = positions.shape
     if len(axes_dims) != axes:
         raise ValueError(f"{axes} axes need {axes} widths, got {len(axes_dims)}")
-    dims, thetas = _axes_arrays(tuple(axes_dims), tuple(theta) if isinstance(theta, (list, tuple)) else theta)
+    # plain numbers: the cache must not go by the identity of something that may change
+    dims, thetas = _axes_arrays(tuple(map(operator.index, axes_dims)),
+                                tuple(map(float, theta)) if isinstance(theta, (list, tuple)) else float(theta))
     return dev, P, axes, int(is_float), dims, thetas
 
 

@@ -159,6 +159,14 @@ def test_valid_calls_without_a_device_report_a_cuda_error():
     assert _add(s, X=far, ldyin=256, ldy=256, Y=ctypes.c_void_p((1 << 20) + 256)) == 4
 
 
+def test_a_batch_without_requests():
+    plan = P.LoraPlan([0], [], [], 5, 3, device="cpu")
+    assert (plan.requests, plan.slots, plan.struct.tiles, plan.struct.groups) == (0, 1, 0, 0)
+    assert plan.sizes()[:4] == P.LoraPlan([0], np.zeros((0, 1), np.int32), np.zeros((0, 1)), 5, 3, device="cpu").sizes()[:4]
+    with pytest.raises(ValueError, match="row_offsets"):
+        P.LoraPlan([0, 4], [0], [1.0, 1.0], 4, 2, device="cpu")
+
+
 def test_python_wrapper_refuses_before_the_call():
     plan = P.LoraPlan([0, 4], [0], [1.0], 4, 2, device="cpu")
     bf = torch.bfloat16

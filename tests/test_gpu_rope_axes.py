@@ -203,3 +203,18 @@ def test_a_graph_reads_new_positions(P):
     assert torch.equal(out, P.svdq_qk_norm_rope(q, None, None, None, 0.0, other, [32, 32], 1e4)[0])
     assert torch.equal(cos, P.svdq_rope_axes_tables(other, [32, 32], 1e4, 64)[0])
     assert P.svdq_device_status() == 0
+
+
+def test_axes_given_as_tensors_are_read_at_every_call(P):
+    pos = _positions(40, 2, False, 3)
+    theta, dims = torch.tensor(1e4), torch.tensor([16, 8])
+    first = P.svdq_rope_axes_tables(pos, dims, theta, 32)[0]
+    assert torch.equal(first, P.svdq_rope_axes_tables(pos, [16, 8], 1e4, 32)[0])
+    theta.fill_(100.0)
+    dims.copy_(torch.tensor([8, 16]))
+    assert torch.equal(P.svdq_rope_axes_tables(pos, dims, theta, 32)[0], P.svdq_rope_axes_tables(pos, [8, 16], 100.0, 32)[0])
+    thetas = [theta, torch.tensor(1e3)]
+    P.svdq_rope_axes_tables(pos, np.array([8, 16]), thetas, 32)
+    thetas[1].fill_(10.0)
+    assert torch.equal(P.svdq_rope_axes_tables(pos, [8, 16], thetas, 32)[0],
+                       P.svdq_rope_axes_tables(pos, [8, 16], [100.0, 10.0], 32)[0])
