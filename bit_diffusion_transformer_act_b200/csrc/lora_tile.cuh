@@ -92,11 +92,13 @@ lora_tile_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_cons
   if (warp == 1) tmem_alloc<kTmemCols>(smem_addr(tmem_slot));
   if (warp == 2 && lane == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(rec_g));   // a hint: L2 is coherent
   grid_dependency_wait();                           // X (or the plan, or an adapter) may come from the previous kernel
-  grid_launch_dependents();                         // kernel 14 counts on this coming after the wait
   if (warp == 2 && lane < 4 + p.slots) rec[lane] = __ldcg(rec_g + lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // Kernel 14 counts on this coming after the wait.  After the allocation too, as in every kernel here that uses
+  // tensor memory: what starts now may take the rest of it and wait for this grid.
+  grid_launch_dependents();
   const uint32_t tmem = *tmem_slot;
   const int row0 = rec[0], nrows = rec[1];
   const int32_t* ids = rec + 4;
