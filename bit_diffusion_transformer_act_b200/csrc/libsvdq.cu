@@ -965,14 +965,21 @@ static int lora_tiles_launch(const LoraCall& c, bool copy) {
     const int room = static_cast<int64_t>(tiles) * p.ks <= sms ? 227 * 1024 : 75 * 1024;
     p.stages = std::min(k13::kMaxStages, (room - k13::kSmemExtra) / k13::stage_bytes(jr));
     const int smem = p.stages * k13::stage_bytes(jr) + k13::kSmemExtra;
-    CUtensorMap tX, tX128, tA;
+    p.N = c.N;
+    p.up_chunks = (c.N + k14::kBN - 1) / k14::kBN;
+    p.up_items = all * p.up_chunks;
+    p.up_ctas = std::min(p.up_items, sms);
+    p.up_ahead = std::min(k13::kYAhead, p.up_items / sms);
+    CUtensorMap tX, tX128, tA, tYin128;
     if (!make_tmap(&tX, c.X, bf, 2, c.M, c.K, k13::kChunk, 32, CU_TENSOR_MAP_SWIZZLE_128B, c.ldx) ||
         !make_tmap(&tX128, c.X, bf, 2, c.M, c.K, k13::kChunk, 128, CU_TENSOR_MAP_SWIZZLE_128B, c.ldx) ||
+        !make_tmap(&tYin128, c.Yin, bf, 2, c.M, c.N, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, c.ldyin) ||
         !make_tmap(&tA, c.A, bf, 2, static_cast<uint64_t>(p.adapters) * c.rank, c.K, k13::kChunk, c.rank,
                    CU_TENSOR_MAP_SWIZZLE_128B) ||
         !set_smem_once<k13::lora_tile_down_kernel>(227 * 1024, c.dev))
       return SVDQ_ERR_CUDA;
-    if (!launch_pdl(k13::lora_tile_down_kernel, dim3(tiles, p.ks), k13::kThreads, smem, 1, c.stream, tX, tX128, tA, p))
+    if (!launch_pdl(k13::lora_tile_down_kernel, dim3(tiles, p.ks), k13::kThreads, smem, 1, c.stream, tX, tX128, tA,
+                    tYin128, p))
       return SVDQ_ERR_CUDA;
   }
   k14::Params p;
