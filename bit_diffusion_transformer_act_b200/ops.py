@@ -633,13 +633,13 @@ def svdq_lora_add(X, Y, A, B, plan, out=None, workspace=None):
     if words.get_device() != dev:
         _require_blob(words, "plan", plan.struct.bytes)
     if out is None:
-        out = Y.new_empty((M, N))
+        out = Y.new_empty(M, N)
         op, ldy = out.data_ptr(), N
     else:
         op, ldy = _row_strided(out, M, N, "out", dev)
     ws_bytes = plan.workspace_bytes(K, rank, dev)
     if workspace is None:
-        workspace = words.new_empty((ws_bytes,))
+        workspace = words.new_empty(ws_bytes)
     else:
         _require_blob(workspace, "workspace", ws_bytes)
     st = LIB.svdq_lora_add(xp, ldx, yp, ldyin, ap, bp, plan.struct_ref, words.data_ptr(), plan.nbytes, M, N, K, rank,
@@ -705,7 +705,7 @@ def _heads_in_out(t, out, w, M, D, name, dev):
         return None, 0, 0, 0, None, None, 0, 0, None
     tp, row, head, heads = _heads(t, M, D, name, dev)
     if out is None:
-        out = t.new_empty((M, heads, D))
+        out = t.new_empty(M, heads, D)
         op, orow, ohead = out.data_ptr(), heads * D, D
     else:
         op, orow, ohead, oheads = _heads(out, M, D, "out_" + name, dev)
@@ -748,7 +748,7 @@ def svdq_rope_axes_tables(positions, axes_dims, theta, head_dim, rows=None, rope
     tables = []
     for t, name in ((rope_cos, "rope_cos"), (rope_sin, "rope_sin")):
         if t is None:
-            t = positions.new_empty(shape, dtype=torch.float32)
+            t = positions.new_empty(*shape, dtype=torch.float32)
             tables.append((t, t.data_ptr()))
         else:
             tables.append((t, _addr(t, torch.float32, shape, name, dev)))
