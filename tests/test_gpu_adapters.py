@@ -238,6 +238,22 @@ def test_many_adapters_in_one_batch(P):
     _check(P.svdq_lora_add(x, y, a, b, P.LoraPlan(off, ids, w, M, M)), x, y, a, b, off, ids, w)
 
 
+@pytest.mark.parametrize("case", [
+    (20011, 128, 192, 64, 2, 3, [0, 7000, 7003, 19900, 20000]),     # more tiles than SMs, slices of one
+    (3001, 256, 2624, 32, 1, 3, [0, 500, 510, 2000, 2900]),         # many pieces per CTA, the last of 64 columns
+], ids=["tiles", "pieces"])
+def test_more_tiles_or_pieces_than_sms(P, case):
+    M, K, N, R, slots, adapters, off = case
+    x, y, a, b = _make(M, K, N, R, slots, adapters)
+    ids = _ids(case)
+    w = _weights(ids)
+    plan = P.LoraPlan(off, ids, w, M, adapters)
+    out = P.svdq_lora_add(x, y, a, b, plan)
+    _check(out, x, y, a, b, off, ids, w)
+    assert torch.equal(P.svdq_lora_add(x, y, a, b, plan, out=y), out)
+    assert P.svdq_device_status() == 0
+
+
 def test_the_output_carries_no_autograd_graph(P):
     """The calls are for inference, as the layers' are: their results are no part of a graph."""
     x, y, a, b = _make(20, 64, 64, 16, 1, 1)
