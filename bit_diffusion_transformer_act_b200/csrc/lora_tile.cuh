@@ -35,7 +35,7 @@ namespace k13 {
 constexpr int kRows = kLoraTileRows;
 constexpr int kChunk = 64;
 constexpr int kThreads = 192;                       // producer, MMA, four read-out warps
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 6;                       // 8 and 12 gave nothing (4608 x 7680, 64 ranks: 35.8, 35.9, 36.5 us)
 constexpr int kYAhead = 3;                          // pieces of y brought to L2 for kernel 14: 36.9 -> 35.7 us at 4608 x
                                                     // 7680, 64 ranks (1: 36.2, 2: 36.0, 4: 35.8, 6: 35.8)
 constexpr int kXBytes = kRows * kChunk * 2;
