@@ -528,6 +528,10 @@ lora_tile_up_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
                          : "r"(yq + h * 16384 + r * 128 + ((c ^ (static_cast<uint32_t>(r) & 7u)) << 4)) : "memory");
             *reinterpret_cast<uint4*>(p.Y + (tile.x + 32 * q + r) * p.ldy + n0 + 64 * h + 8 * c) = v;
           }
+        // TMA refills the stage: the warp's writes of the sums are ordered before that (another proxy), and every
+        // lane has read what it stores (lanes leave the loop at different rows) before lane 0 hands the stage back.
+        fence_proxy_async_smem();
+        __syncwarp();
       }
       if (lane == 0) {                              // hand the stage back once its store has read it
         bulk_commit_group();

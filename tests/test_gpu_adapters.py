@@ -276,3 +276,28 @@ def test_device_and_stream(P):
     _check(out, x, y, a, b, off, ids, w)
     with pytest.raises(ValueError, match="CUDA tensor"):
         P.svdq_lora_add(x, y, a, b, P.LoraPlan(off, ids, w, 200, 2, device="cpu"))
+
+
+@pytest.mark.parametrize("rows", [17, 31, 47, 63, 97, 127])
+def test_partial_slabs_through_a_turning_ring(P, rows):
+    """Tiles that end inside a 32-row slab are stored row by row from a stage that TMA then refills; with more
+    pieces per CTA than stages every stage is refilled.  The rows are those of whole slabs, bit for bit: a row's
+    sums do not depend on its tile (as many tiles, so K is split alike)."""
+    n, K, N, whole = 40, 128, 5120, (rows + 31) // 32 * 32
+    x, y, a, b = _make(n * whole, K, N, 32, 1, 3)
+    ids = np.arange(n)[:, None] % 3
+    w = _weights(ids)
+    expect = P.svdq_lora_add(x, y, a, b, P.LoraPlan(whole * np.arange(n + 1), ids, w, n * whole, 3))
+
+    def short(t):
+        return t.view(n, whole, -1)[:, :rows].reshape(n * rows, -1).contiguous()
+
+    plan = P.LoraPlan(rows * np.arange(n + 1), ids, w, n * rows, 3)
+    xs, ys = short(x), short(y)
+    for _ in range(10):
+        assert torch.equal(P.svdq_lora_add(xs, ys, a, b, plan), short(expect))
+        in_place = ys.clone()
+        assert torch.equal(P.svdq_lora_add(xs, in_place, a, b, plan, out=in_place), short(expect))
+    off = rows * np.arange(n + 1)
+    _check(short(expect), xs, ys, a, b, off, ids, w)
+    assert P.svdq_device_status() == 0
