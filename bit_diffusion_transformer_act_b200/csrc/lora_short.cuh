@@ -71,18 +71,20 @@ lora_short_down_kernel(const Params p) {
     const __nv_bfloat16* a_hi = a_lo + static_cast<size_t>(8) * p.K;
     const __nv_bfloat16* x_lo = g < nrows ? p.X + rec[12 + g] * p.ldx + 8 * t : nullptr;
     const __nv_bfloat16* x_hi = g + 8 < nrows ? p.X + rec[12 + g + 8] * p.ldx + 8 * t : nullptr;
+    // Ordinary loads: X, or an adapter, may have been written while this grid was already resident, which the
+    // read-only path (ld.global.nc, __ldg) does not allow.
     const int steps = p.K / 32;
     const int end = static_cast<int>(static_cast<long long>(steps) * (blockIdx.z + 1) / p.ks);
 #pragma unroll 4
     for (int s = static_cast<int>(static_cast<long long>(steps) * blockIdx.z / p.ks) + warp; s < end; s += kWarps) {
       const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-      const uint4 al = __ldg(reinterpret_cast<const uint4*>(a_lo + 32 * s));
-      const uint4 ah = __ldg(reinterpret_cast<const uint4*>(a_hi + 32 * s));
-      const uint4 xl = x_lo ? __ldg(reinterpret_cast<const uint4*>(x_lo + 32 * s)) : z;
+      const uint4 al = *reinterpret_cast<const uint4*>(a_lo + 32 * s);
+      const uint4 ah = *reinterpret_cast<const uint4*>(a_hi + 32 * s);
+      const uint4 xl = x_lo ? *reinterpret_cast<const uint4*>(x_lo + 32 * s) : z;
       mma16816(d[0], al.x, ah.x, al.y, ah.y, xl.x, xl.y);
       mma16816(d[0], al.z, ah.z, al.w, ah.w, xl.z, xl.w);
       if (nrows > 8) {
-        const uint4 xh = x_hi ? __ldg(reinterpret_cast<const uint4*>(x_hi + 32 * s)) : z;
+        const uint4 xh = x_hi ? *reinterpret_cast<const uint4*>(x_hi + 32 * s) : z;
         mma16816(d[1], al.x, ah.x, al.y, ah.y, xh.x, xh.y);
         mma16816(d[1], al.z, ah.z, al.w, ah.w, xh.z, xh.w);
       }

@@ -92,16 +92,18 @@ __device__ __forceinline__ void sincos_turns(uint32_t frac, float bad, float& s,
   c = __uint_as_float(__float_as_uint(b) ^ (((q + 1u) & 2u) << 30));
 }
 
-// A position; a float one that is not finite has no angle: `bad` is NaN for it, else 0.
+// A position; a float one that is not finite has no angle: `bad` is NaN for it, else 0.  (An ordinary load: the
+// previous kernel may have written the positions while this grid was already resident, which the read-only path,
+// ld.global.nc, does not allow.)
 template <bool kFloat>
 __device__ __forceinline__ Position<kFloat> position(const void* pos, long long i, float& bad) {
   if constexpr (kFloat) {
-    const float x = __ldg(static_cast<const float*>(pos) + i);
+    const float x = static_cast<const float*>(pos)[i];
     bad = x * 0.f;
     return static_cast<double>(x);
   } else {
     bad = 0.f;
-    return __ldg(static_cast<const int*>(pos) + i);
+    return static_cast<const int*>(pos)[i];
   }
 }
 

@@ -131,3 +131,35 @@ def test_adapters_beside_the_awq_layer(P, rows):
     x = bf(a.X)
     ref, us, ks = oadapters.forward(_np(x), _np(base(x)), _np(layer.A), _np(layer.B), list(range(rows + 1)), ids, wt)
     assert (np.abs(_np(layer(x)) - ref) <= oadapters.bound(ref, us, ks, 512, 16)).all()
+
+
+def test_adapters_read_what_the_kernel_before_them_wrote(P):
+    """X comes from the call just before, whose kernel lets the next one start early: ten pairs of calls over one
+    buffer, without a wait between them, against the same pairs one by one."""
+    M, H = 16, 4
+    g = torch.Generator(device="cuda").manual_seed(6)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+
+    q, y = normal(10, M, H, D), normal(M, 256)
+    a, b = normal(2, 16, H * D), normal(2, 256, 16)
+    pos = torch.arange(3 * M, dtype=torch.int32, device="cuda").view(M, 3)
+    plan = P.LoraPlan([0, 1, M], [1, 0], [0.5, 1.0], M, 2)
+    x = torch.empty((M, H * D), dtype=torch.bfloat16, device="cuda")
+
+    def pair(i):
+        P.svdq_qk_norm_rope(q[i], None, None, None, 0.0, pos, DIMS, THETA, out_q=x.view(M, H, D))
+        return P.svdq_lora_add(x, y, a, b, plan)
+
+    alone = []
+    for i in range(10):
+        alone.append(pair(i))
+        torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        replayed = [pair(i) for i in range(10)]
+    graph.replay()
+    for outs in ([pair(i) for i in range(10)], replayed):
+        assert all(torch.equal(o, e) for o, e in zip(outs, alone))
+    assert not torch.equal(alone[0], alone[1])
