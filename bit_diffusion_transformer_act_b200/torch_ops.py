@@ -16,11 +16,14 @@ Operators (all tensors on one CUDA device):
   svdq::awq_w4a16_linear(X bf16 [M,K], qweight u8 [N,K/2], scales bf16 [N,K/64],
       zeros bf16 [N,K/64], bias bf16 [N] or None) -> Y bf16 [M,N]
   svdq::lora_add_(X bf16 [M,K], Y bf16 [M,N], A bf16 [adapters,rank,K], B bf16 [adapters,N,rank],
-      plan u8, plan_sizes int[9]) -> (), adds each request's adapters to Y
+      plan u8, plan_sizes int[9]) -> (), adds each request's adapters to Y; refuses tensors that carry gradients
+  svdq::lora_add(the same) -> Y' bf16 [M,N], Y left as it is
   svdq::qk_norm_rope(q bf16 [M,Hq,D], k bf16 [M,Hk,D], norm_wq, norm_wk bf16 [D] or None, eps float,
       positions int32 or fp32 [P,axes], axes_dims int[], theta float[], pairing str) -> (q', k')
   svdq::rope_axes_tables(positions, axes_dims int[], theta float[], head_dim int, rows int)
       -> (cos, sin fp32 [head_dim/2, rows])
+
+They are for inference: none has a gradient, and a backward pass through any of them raises.
 """
 
 from typing import Callable, List, Optional, Sequence, Tuple
@@ -83,6 +86,59 @@ def lora_add_(X: torch.Tensor, Y: torch.Tensor, A: torch.Tensor, B: torch.Tensor
 @lora_add_.register_fake
 def _(X, Y, A, B, plan, plan_sizes):
     return None
+
+
+def _carries_gradients(*tensors: torch.Tensor) -> bool:
+    return torch.is_grad_enabled() and any(t.requires_grad for t in tensors)
+
+
+def _lora_add_no_graph(X, Y, A, B, plan, plan_sizes):
+    # An operator that changes its argument can have no gradient formula, and without one Y would keep the gradient of
+    # what it was before: the adapters' part would be missing from it without an error.
+    if _carries_gradients(X, Y, A, B):
+        raise RuntimeError("svdq::lora_add_ has no gradient: call it under torch.no_grad(), on detached tensors, or "
+                           "use svdq::lora_add")
+    with torch._C._AutoDispatchBelowAutograd():
+        torch.ops.svdq.lora_add_.default(X, Y, A, B, plan, plan_sizes)
+
+
+_LIB = torch.library.Library("svdq", "FRAGMENT")
+_LIB.impl("lora_add_", _lora_add_no_graph, "Autograd", allow_override=True)
+
+
+@torch.library.custom_op("svdq::lora_add", mutates_args=())
+def lora_add(X: torch.Tensor, Y: torch.Tensor, A: torch.Tensor, B: torch.Tensor, plan: torch.Tensor,
+             plan_sizes: List[int]) -> torch.Tensor:
+    return ops.svdq_lora_add(X, Y, A, B, ops.LoraPlan.from_parts(plan, plan_sizes))
+
+
+@lora_add.register_fake
+def _(X, Y, A, B, plan, plan_sizes):
+    return Y.new_empty(Y.shape)
+
+
+@torch.library.custom_op("svdq::no_gradient", mutates_args=())
+def no_gradient(grad: torch.Tensor, shape: List[int], name: str) -> torch.Tensor:
+    """Stands for a gradient that there is none of.  An operator, so that a compiled forward pass runs and only the
+    backward pass raises."""
+    raise RuntimeError(f"{name} has no gradient (the adapters are for inference): run it under torch.no_grad()")
+
+
+@no_gradient.register_fake
+def _(grad, shape, name):
+    return grad.new_empty(shape)
+
+
+def _lora_add_context(ctx, inputs, output):
+    ctx.shapes = [t.shape for t in inputs[:4]]
+
+
+def _lora_add_backward(ctx, grad):
+    return tuple(no_gradient(grad, list(shape), "svdq::lora_add") if need else None
+                 for need, shape in zip(ctx.needs_input_grad, ctx.shapes)) + (None, None)
+
+
+lora_add.register_autograd(_lora_add_backward, setup_context=_lora_add_context)
 
 
 @torch.library.custom_op("svdq::qk_norm_rope", mutates_args=())
@@ -201,7 +257,8 @@ class LoraLinear(nn.Module):
 
     A bf16 [adapters, rank, in_features], B bf16 [adapters, out_features, rank].  Which rows use which adapters is
     the batch's plan (``set_plan``; rows are counted after flattening the leading dimensions); without a plan
-    the layer is its base.  For inference: no gradients."""
+    the layer is its base.  For inference: a backward pass through the adapters raises.  (The adapters are added to
+    the base's output in place, into a copy only where gradients are on and something carries them.)"""
 
     def __init__(self, base: nn.Module, A: torch.Tensor, B: torch.Tensor):
         super().__init__()
@@ -239,8 +296,11 @@ class LoraLinear(nn.Module):
         y = self.base(x)
         if self.plan_words is None:
             return y
-        y2 = y.reshape(-1, self.out_features)
-        torch.ops.svdq.lora_add_(_as_2d(x, self.in_features), y2, self.A, self.B, self.plan_words, self.plan_sizes)
+        x2, y2 = _as_2d(x, self.in_features), y.reshape(-1, self.out_features)
+        if _carries_gradients(x2, y2, self.A, self.B):
+            y2 = torch.ops.svdq.lora_add(x2, y2, self.A, self.B, self.plan_words, self.plan_sizes)
+        else:
+            torch.ops.svdq.lora_add_(x2, y2, self.A, self.B, self.plan_words, self.plan_sizes)
         return y2.reshape(y.shape)
 
     def extra_repr(self) -> str:

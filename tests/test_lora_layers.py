@@ -73,3 +73,77 @@ def test_state_dict_carries_the_pool():
     a, b = T.LoraLinear.from_adapters(_awq(), _pool()), T.LoraLinear.from_adapters(_awq(), _pool(ranks=(1, 1, 32)))
     b.load_state_dict(a.state_dict())
     assert torch.equal(a.A, b.A) and torch.equal(a.B, b.B)
+
+
+@pytest.fixture
+def host_kernel(monkeypatch):
+    """The adapters' call computed on the host, behind the real operators; returns the calls' modes."""
+    calls = []
+
+    def add(X, Y, A, B, plan, out=None, workspace=None):
+        calls.append("new" if out is None else "in place")
+        r = Y.detach().clone()
+        w = plan.words.view(torch.int32)
+        assert plan.struct.tiles == 0 and plan.struct.slots == 1
+        for g in w[16:].view(-1, 44)[: plan.struct.groups]:
+            for i in range(int(g[0])):
+                m, wt = int(g[12 + i]), g[28 + i: 29 + i].view(torch.float32)
+                r[m] += (wt * (B[g[4]].float() @ (A[g[4]].float() @ X.detach()[m].float()))).to(torch.bfloat16)
+        if out is None:
+            return r
+        out.detach().copy_(r)
+        return out
+
+    monkeypatch.setattr(T.ops, "svdq_lora_add", add)
+    monkeypatch.setattr(T.ops, "_on_device", lambda t, name: None)
+    return calls
+
+
+def _linear_layer(K=64, N=128):
+    torch.manual_seed(0)
+    base = nn.Linear(K, N).to(torch.bfloat16)
+    layer = T.LoraLinear.from_adapters(base, [(torch.randn(4, K), torch.randn(N, 4)) for _ in range(2)])
+    layer.set_plan(P.LoraPlan([0, 2, 3], [1, 0], [0.5, 2.0], 4, 2, device="cpu"))
+    return base, layer
+
+
+@pytest.mark.parametrize("compiled", [False, True])
+def test_a_backward_pass_through_adapters_raises(host_kernel, compiled):
+    """It dropped the adapters' part of the gradient: the in-place sum left the base's graph as it was."""
+    base, layer = _linear_layer()
+    run = torch.compile(layer, fullgraph=True, backend="aot_eager") if compiled else layer
+    x = torch.randn(4, 64).to(torch.bfloat16)
+    with torch.no_grad():
+        expect = run(x)
+    assert not torch.equal(expect, base(x)) and host_kernel == ["in place"]
+    for x_grad, w_grad in ((True, True), (True, False), (False, True)):
+        base.requires_grad_(w_grad)
+        y = run(x.clone().requires_grad_(x_grad))
+        assert y.requires_grad and torch.equal(y, expect) and host_kernel[-1] == "new"
+        with pytest.raises(RuntimeError, match="no gradient"):
+            y.float().sum().backward()
+    with torch.no_grad():
+        assert torch.equal(run(x), expect) and host_kernel[-1] == "in place"
+
+
+def test_the_in_place_operator_refuses_gradients(host_kernel):
+    base, layer = _linear_layer()
+    x = torch.randn(4, 64).to(torch.bfloat16)
+
+    def add(x, y):
+        torch.ops.svdq.lora_add_(x, y, layer.A, layer.B, layer.plan_words, layer.plan_sizes)
+        return y
+
+    with pytest.raises(RuntimeError, match="no gradient"):
+        add(x, base(x))
+    with pytest.raises(RuntimeError, match="no gradient"):
+        add(x.clone().requires_grad_(), base(x).detach())
+    assert host_kernel == []
+    y = base(x).detach()
+    before = y._version
+    expect = add(x, y).clone()
+    assert y._version > before
+    with torch.no_grad():
+        assert torch.equal(add(x.clone().requires_grad_(), base(x)), expect)
+    with torch.inference_mode():
+        assert torch.equal(add(x, base(x)), expect)
