@@ -143,6 +143,20 @@ def _addr(t, dtype, shape, name, dev):
     return t.data_ptr()
 
 
+def _writable(t, name):
+    """Refuses an output tensor that the calling code differentiates: the call writes through its address, which
+    its graph would not know of."""
+    if torch.is_grad_enabled() and getattr(t, "requires_grad", False):
+        raise ValueError(f"{name} carries gradients, which this call has none of: call it under torch.no_grad(), or on "
+                         "a detached tensor")
+
+
+def _written(*tensors):
+    """Counts the call's writes to tensors of the caller's, so that a graph that saved one of them notices."""
+    for t in tensors:
+        torch.autograd.graph.increment_version(t)
+
+
 def _l1_section_end(K, rank):
     """Bytes of the packed blob that the activation kernel reads: the 1 KB header and the
     low-rank down factor section that follows it (two bf16 [rank, K] parts, hi and lo).  The C
@@ -615,9 +629,10 @@ def svdq_lora_add(X, Y, A, B, plan, out=None, workspace=None):
 
     X bf16 [M, K], Y bf16 [M, N] (a projection's output for X), rows possibly strided; A bf16
     [adapters, rank, K], B bf16 [adapters, N, rank].  out: Y itself for in place, a [M, N] tensor that
-    overlaps neither, or None for a new one.  Returns out."""
+    overlaps neither, or None for a new one.  Returns out, which is no part of an autograd graph."""
     if not isinstance(plan, LoraPlan):
         raise ValueError("plan must be a LoraPlan")
+    _writable(out, "out")
     M, K = X.shape
     adapters, rank, _ = A.shape
     N = Y.shape[1]
@@ -632,11 +647,12 @@ def svdq_lora_add(X, Y, A, B, plan, out=None, workspace=None):
     words = plan.words
     if words.get_device() != dev:
         _require_blob(words, "plan", plan.struct.bytes)
-    if out is None:
+    given = out is not None
+    if given:
+        op, ldy = _row_strided(out, M, N, "out", dev)
+    else:
         out = Y.new_empty(M, N)
         op, ldy = out.data_ptr(), N
-    else:
-        op, ldy = _row_strided(out, M, N, "out", dev)
     ws_bytes = plan.workspace_bytes(K, rank, dev)
     if workspace is None:
         workspace = words.new_empty(ws_bytes)
@@ -646,6 +662,8 @@ def svdq_lora_add(X, Y, A, B, plan, out=None, workspace=None):
                            workspace.data_ptr(), workspace.numel(), op, ldy, torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _check("svdq_lora_add", st)
+    if given:
+        _written(out)
     return out
 
 
@@ -722,9 +740,12 @@ def svdq_qk_norm_rope(q, k, norm_wq, norm_wk, eps, positions, axes_dims, theta, 
     norm_wq / norm_wk bf16 [D] or None for no normalisation, positions int32 or float32 [P, axes]
     (token m has position m % P), axes_dims the rotated columns of each axis, theta one value or one per axis,
     pairing "interleaved" or "half".  out_q / out_k: q / k themselves for in place, tensors of their
-    shape, or None for new ones.  Returns (out_q, out_k)."""
+    shape, or None for new ones.  Returns (out_q, out_k), which are no part of an autograd graph."""
     if q is None and k is None:
         raise ValueError("q or k is needed")
+    _writable(out_q, "out_q")
+    _writable(out_k, "out_k")
+    given = [t for t in (out_q, out_k) if t is not None]
     M, _, D = (q if q is not None else k).shape
     dev, P, axes, is_float, dims, thetas = _rope_axes(positions, axes_dims, theta)
     if pairing not in _PAIRINGS:
@@ -736,6 +757,7 @@ def svdq_qk_norm_rope(q, k, norm_wq, norm_wk, eps, positions, axes_dims, theta, 
                                torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _check("svdq_qk_norm_rope", st)
+    _written(*given)
     return out_q, out_k
 
 
@@ -745,18 +767,21 @@ def svdq_rope_axes_tables(positions, axes_dims, theta, head_dim, rows=None, rope
     dev, P, axes, is_float, dims, thetas = _rope_axes(positions, axes_dims, theta)
     M = P if rows is None else rows
     shape = (head_dim // 2, M)
-    tables = []
+    tables, given = [], []
     for t, name in ((rope_cos, "rope_cos"), (rope_sin, "rope_sin")):
         if t is None:
             t = positions.new_empty(*shape, dtype=torch.float32)
             tables.append((t, t.data_ptr()))
         else:
+            _writable(t, name)
+            given.append(t)
             tables.append((t, _addr(t, torch.float32, shape, name, dev)))
     (rope_cos, cp), (rope_sin, sp) = tables
     st = LIB.svdq_rope_axes_tables(positions.data_ptr(), is_float, P, axes, dims, thetas, M, head_dim, cp, sp,
                                    torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _check("svdq_rope_axes_tables", st)
+    _written(*given)
     return rope_cos, rope_sin
 
 

@@ -163,3 +163,29 @@ def test_adapters_read_what_the_kernel_before_them_wrote(P):
     for outs in ([pair(i) for i in range(10)], replayed):
         assert all(torch.equal(o, e) for o, e in zip(outs, alone))
     assert not torch.equal(alone[0], alone[1])
+
+
+def test_writes_to_given_tensors_are_counted(P):
+    """A graph that has saved a tensor notices when a call writes to it."""
+    def normal(*shape):
+        return torch.randn(shape, device="cuda").to(torch.bfloat16)
+
+    plan = P.LoraPlan([0, 8], [0], [1.0], 8, 1)
+    x, y, a, b = normal(8, 64), normal(8, 128), normal(1, 16, 64), normal(1, 128, 16)
+    pos = torch.ones((8, 1), dtype=torch.int32, device="cuda")
+    q, k = normal(8, 2, 64), normal(8, 2, 64)
+    cos, sin = torch.empty((2, 32, 8), device="cuda").unbind(0)
+    for write, tensors in ((lambda: P.svdq_lora_add(x, y, a, b, plan, out=y), [y]),
+                           (lambda: P.svdq_qk_norm_rope(q, k, None, None, 0.0, pos, [64], 1e4, out_q=q, out_k=k), [q, k]),
+                           (lambda: P.svdq_rope_axes_tables(pos, [64], 1e4, 64, 8, cos, sin), [cos, sin])):
+        before = [t._version for t in tensors]
+        write()
+        assert all(t._version > v for t, v in zip(tensors, before))
+    w = torch.randn((8, 128), device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    z = w * y                                           # keeps y
+    P.svdq_lora_add(x, y, a, b, plan, out=y)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        z.float().sum().backward()
+    with torch.inference_mode():
+        t = y.clone()
+        assert P.svdq_lora_add(x, t, a, b, plan, out=t) is t

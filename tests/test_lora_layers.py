@@ -147,3 +147,21 @@ def test_the_in_place_operator_refuses_gradients(host_kernel):
         assert torch.equal(add(x.clone().requires_grad_(), base(x)), expect)
     with torch.inference_mode():
         assert torch.equal(add(x, base(x)), expect)
+
+
+def test_calls_refuse_an_output_that_carries_gradients():
+    """They write through its address: its graph would go on as if it had kept its values."""
+    bf = torch.bfloat16
+    plan = P.LoraPlan([0, 4], [0], [1.0], 4, 2, device="cpu")
+    x, a, b = torch.zeros((4, 64), dtype=bf), torch.zeros((2, 16, 64), dtype=bf), torch.zeros((2, 128, 16), dtype=bf)
+    y = torch.zeros((4, 128), dtype=bf, requires_grad=True) * 2
+    with pytest.raises(ValueError, match="out carries gradients"):
+        P.svdq_lora_add(x, y, a, b, plan, out=y)
+    pos = torch.zeros((4, 2), dtype=torch.int32)
+    q = y.view(4, 2, 64)
+    with pytest.raises(ValueError, match="out_q carries gradients"):
+        P.svdq_qk_norm_rope(q, None, None, None, 0.0, pos, [32, 32], 1e4, out_q=q)
+    with pytest.raises(ValueError, match="out_k carries gradients"):
+        P.svdq_qk_norm_rope(None, q, None, None, 0.0, pos, [32, 32], 1e4, out_k=q)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA tensor"):      # past that check
+        P.svdq_lora_add(x, y, a, b, plan, out=y)
