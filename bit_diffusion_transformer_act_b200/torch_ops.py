@@ -17,7 +17,9 @@ Operators (all tensors on one CUDA device):
       zeros bf16 [N,K/64], bias bf16 [N] or None) -> Y bf16 [M,N]
   svdq::lora_add_(X bf16 [M,K], Y bf16 [M,N], A bf16 [adapters,rank,K], B bf16 [adapters,N,rank],
       plan u8, plan_sizes int[9]) -> (), adds each request's adapters to Y; refuses tensors that carry gradients
-  svdq::lora_add(the same) -> Y' bf16 [M,N], Y left as it is
+  svdq::lora_add_planned_(the same, plan_sizes int64 [9] on the host): the sizes as data, which a compiled graph
+      does not depend on
+  svdq::lora_add(as lora_add_planned_) -> Y' bf16 [M,N], Y left as it is
   svdq::qk_norm_rope(q bf16 [M,Hq,D], k bf16 [M,Hk,D], norm_wq, norm_wk bf16 [D] or None, eps float,
       positions int32 or fp32 [P,axes], axes_dims int[], theta float[], pairing str) -> (q', k')
   svdq::rope_axes_tables(positions, axes_dims int[], theta float[], head_dim int, rows int)
@@ -92,24 +94,43 @@ def _carries_gradients(*tensors: torch.Tensor) -> bool:
     return torch.is_grad_enabled() and any(t.requires_grad for t in tensors)
 
 
-def _lora_add_no_graph(X, Y, A, B, plan, plan_sizes):
-    # An operator that changes its argument can have no gradient formula, and without one Y would keep the gradient of
-    # what it was before: the adapters' part would be missing from it without an error.
-    if _carries_gradients(X, Y, A, B):
-        raise RuntimeError("svdq::lora_add_ has no gradient: call it under torch.no_grad(), on detached tensors, or "
-                           "use svdq::lora_add")
-    with torch._C._AutoDispatchBelowAutograd():
-        torch.ops.svdq.lora_add_.default(X, Y, A, B, plan, plan_sizes)
+# The launches follow from plan_sizes' values, which inductor's CUDA graphs would keep from the first plan.
+_READS_HOST_VALUES = (torch.Tag.cudagraph_unsafe,)
+
+
+@torch.library.custom_op("svdq::lora_add_planned_", mutates_args={"Y"}, tags=_READS_HOST_VALUES)
+def lora_add_planned_(X: torch.Tensor, Y: torch.Tensor, A: torch.Tensor, B: torch.Tensor, plan: torch.Tensor,
+                      plan_sizes: torch.Tensor) -> None:
+    ops.svdq_lora_add(X, Y, A, B, ops.LoraPlan.from_parts(plan, plan_sizes.tolist()), out=Y)
+
+
+@lora_add_planned_.register_fake
+def _(X, Y, A, B, plan, plan_sizes):
+    return None
+
+
+# An operator that changes its argument can have no gradient formula, and without one Y would keep the gradient of
+# what it was before: the adapters' part would be missing from it without an error.
+def _refuse_gradients(op):
+    def call(X, Y, A, B, plan, plan_sizes):
+        if _carries_gradients(X, Y, A, B):
+            raise RuntimeError(f"{op} has no gradient: call it under torch.no_grad(), on detached tensors, or use "
+                               "svdq::lora_add")
+        with torch._C._AutoDispatchBelowAutograd():
+            op(X, Y, A, B, plan, plan_sizes)
+    return call
 
 
 _LIB = torch.library.Library("svdq", "FRAGMENT")
-_LIB.impl("lora_add_", _lora_add_no_graph, "Autograd", allow_override=True)
+_LIB.impl("lora_add_", _refuse_gradients(torch.ops.svdq.lora_add_.default), "Autograd", allow_override=True)
+_LIB.impl("lora_add_planned_", _refuse_gradients(torch.ops.svdq.lora_add_planned_.default), "Autograd",
+          allow_override=True)
 
 
-@torch.library.custom_op("svdq::lora_add", mutates_args=())
+@torch.library.custom_op("svdq::lora_add", mutates_args=(), tags=_READS_HOST_VALUES)
 def lora_add(X: torch.Tensor, Y: torch.Tensor, A: torch.Tensor, B: torch.Tensor, plan: torch.Tensor,
-             plan_sizes: List[int]) -> torch.Tensor:
-    return ops.svdq_lora_add(X, Y, A, B, ops.LoraPlan.from_parts(plan, plan_sizes))
+             plan_sizes: torch.Tensor) -> torch.Tensor:
+    return ops.svdq_lora_add(X, Y, A, B, ops.LoraPlan.from_parts(plan, plan_sizes.tolist()))
 
 
 @lora_add.register_fake
@@ -257,7 +278,9 @@ class LoraLinear(nn.Module):
 
     A bf16 [adapters, rank, in_features], B bf16 [adapters, out_features, rank].  Which rows use which adapters is
     the batch's plan (``set_plan``; rows are counted after flattening the leading dimensions); without a plan
-    the layer is its base.  For inference: a backward pass through the adapters raises.  (The adapters are added to
+    the layer is its base.  A compiled layer takes one plan after another without being compiled again: the plan's
+    sizes are data, in a small host tensor (and inductor's CUDA graphs leave the adapters' calls out: the number of
+    blocks launched follows from the sizes).  For inference: a backward pass through the adapters raises.  (The adapters are added to
     the base's output in place, into a copy only where gradients are on and something carries them.)"""
 
     def __init__(self, base: nn.Module, A: torch.Tensor, B: torch.Tensor):
@@ -271,7 +294,7 @@ class LoraLinear(nn.Module):
         self.register_buffer("A", A)
         self.register_buffer("B", B)
         self.plan_words: Optional[torch.Tensor] = None
-        self.plan_sizes: List[int] = []
+        self.plan_sizes: Optional[torch.Tensor] = None
 
     @classmethod
     def from_adapters(cls, base: nn.Module, adapters: Sequence[Tuple[torch.Tensor, torch.Tensor]]) -> "LoraLinear":
@@ -289,8 +312,12 @@ class LoraLinear(nn.Module):
         return cls(base, A, B)
 
     def set_plan(self, plan: Optional[ops.LoraPlan]) -> None:
-        self.plan_words = None if plan is None else plan.words
-        self.plan_sizes = [] if plan is None else plan.sizes()
+        if plan is None:
+            self.plan_words = self.plan_sizes = None
+            return
+        self.plan_words = plan.words
+        self.plan_sizes = torch.tensor(plan.sizes(), dtype=torch.int64)
+        torch._dynamo.maybe_mark_dynamic(self.plan_words, 0)   # plans differ in length
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         y = self.base(x)
@@ -300,7 +327,7 @@ class LoraLinear(nn.Module):
         if _carries_gradients(x2, y2, self.A, self.B):
             y2 = torch.ops.svdq.lora_add(x2, y2, self.A, self.B, self.plan_words, self.plan_sizes)
         else:
-            torch.ops.svdq.lora_add_(x2, y2, self.A, self.B, self.plan_words, self.plan_sizes)
+            torch.ops.svdq.lora_add_planned_(x2, y2, self.A, self.B, self.plan_words, self.plan_sizes)
         return y2.reshape(y.shape)
 
     def extra_repr(self) -> str:

@@ -189,3 +189,41 @@ def test_writes_to_given_tensors_are_counted(P):
     with torch.inference_mode():
         t = y.clone()
         assert P.svdq_lora_add(x, t, a, b, plan, out=t) is t
+
+
+def test_a_compiled_layer_over_many_plans(P, block):
+    w, base, layer, x, pos, nq, nk = block
+    torch._dynamo.reset()
+    compiles = []
+
+    def backend(gm, inputs):
+        compiles.append(1)
+        return gm.forward
+
+    run = torch.compile(layer, fullgraph=True, backend=backend)
+    for i in range(12):
+        off = [0] + sorted({1 + 7 * i, 20 + 13 * i, 290 - 9 * i})
+        n = len(off) - 1
+        ids, wt = np.arange(i, i + n)[:, None] % 4 - 1, np.linspace(-1, 1, n, dtype=np.float32)[:, None]
+        plan = P.LoraPlan(off, ids, wt, 300, 3)
+        layer.set_plan(plan)
+        assert torch.equal(run(x), P.svdq_lora_add(x, base(x), layer.A, layer.B, plan))
+    assert len(compiles) == 1
+
+
+def test_inductors_cuda_graphs_do_not_keep_a_plan(P):
+    """Two plans of the same length in memory that launch different numbers of blocks."""
+    torch._dynamo.reset()
+    base = torch.nn.Linear(256, 192, device="cuda").to(torch.bfloat16).requires_grad_(False)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    layer = P.LoraLinear.from_adapters(base, [(torch.randn((16, 256), generator=g, device="cuda"),
+                                               torch.randn((192, 16), generator=g, device="cuda"))])
+    plans = [P.LoraPlan([0, 200], [0], [1.0], 300, 1), P.LoraPlan([0, 100], [0], [1.0], 300, 1)]
+    assert plans[0].nbytes == plans[1].nbytes and plans[0].struct.tiles != plans[1].struct.tiles
+    run = torch.compile(layer, fullgraph=True, mode="reduce-overhead")
+    with torch.no_grad():
+        for i in range(8):
+            x = torch.randn((300, 256), generator=g, device="cuda").to(torch.bfloat16)
+            plan = plans[i // 4]
+            layer.set_plan(plan)
+            assert torch.equal(run(x).clone(), P.svdq_lora_add(x, base(x), layer.A, layer.B, plan))

@@ -85,7 +85,7 @@ def host_kernel(monkeypatch):
         r = Y.detach().clone()
         w = plan.words.view(torch.int32)
         assert plan.struct.tiles == 0 and plan.struct.slots == 1
-        for g in w[16:].view(-1, 44)[: plan.struct.groups]:
+        for g in w[16 + 8 * plan.struct.copy_tiles:].view(-1, 44)[: plan.struct.groups]:
             for i in range(int(g[0])):
                 m, wt = int(g[12 + i]), g[28 + i: 29 + i].view(torch.float32)
                 r[m] += (wt * (B[g[4]].float() @ (A[g[4]].float() @ X.detach()[m].float()))).to(torch.bfloat16)
@@ -128,10 +128,11 @@ def test_a_backward_pass_through_adapters_raises(host_kernel, compiled):
 
 def test_the_in_place_operator_refuses_gradients(host_kernel):
     base, layer = _linear_layer()
+    plan = P.LoraPlan([0, 2, 3], [1, 0], [0.5, 2.0], 4, 2, device="cpu")
     x = torch.randn(4, 64).to(torch.bfloat16)
 
     def add(x, y):
-        torch.ops.svdq.lora_add_(x, y, layer.A, layer.B, layer.plan_words, layer.plan_sizes)
+        torch.ops.svdq.lora_add_(x, y, layer.A, layer.B, plan.words, plan.sizes())
         return y
 
     with pytest.raises(RuntimeError, match="no gradient"):
@@ -165,3 +166,29 @@ def test_calls_refuse_an_output_that_carries_gradients():
         P.svdq_qk_norm_rope(None, q, None, None, 0.0, pos, [32, 32], 1e4, out_k=q)
     with torch.no_grad(), pytest.raises(ValueError, match="CUDA tensor"):      # past that check
         P.svdq_lora_add(x, y, a, b, plan, out=y)
+
+
+def test_one_compiled_graph_serves_every_plan(host_kernel):
+    """The plan's sizes were guarded on one by one: every batch compiled again, and the ninth raised."""
+    base, layer = _linear_layer()
+    torch._dynamo.reset()
+    compiles = []
+
+    def backend(gm, inputs):
+        compiles.append(1)
+        return gm.forward
+
+    run = torch.compile(layer, fullgraph=True, backend=backend)
+    x = torch.randn(40, 64).to(torch.bfloat16)
+    sizes = set()
+    with torch.no_grad():
+        for i in range(20):
+            n = 1 + i * 2 % 13
+            off = [min(40, 3 * r * (1 + i % 2)) for r in range(n + 1)]
+            plan = P.LoraPlan(off, [r % 3 - 1 for r in range(n)], [0.25 * i + r for r in range(n)], 40, 2, device="cpu")
+            sizes.add(tuple(plan.sizes()))
+            layer.set_plan(plan)
+            assert torch.equal(run(x), layer(x))
+        assert len(sizes) > 15 and len(compiles) == 1
+        layer.set_plan(None)
+        assert torch.equal(run(x), base(x)) and len(compiles) == 2
