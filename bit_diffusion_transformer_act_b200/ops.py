@@ -545,6 +545,9 @@ def _int32_array(v, name):
     return np.ascontiguousarray(a, dtype=np.int32)
 
 
+LORA_MAX_RANK = 128                     # of slots * rank
+
+
 class LoraPlan:
     """The plan of a batch whose requests carry low-rank adapters (svdq_lora_plan_pack): which rows belong
     to which request, which adapters each has, and how strongly.  One plan serves every layer and

@@ -276,12 +276,13 @@ class LoraLinear(nn.Module):
     """A shared projection (an SvdqLinear, an AwqLinear, an nn.Linear) with a pool of low-rank adapters beside
     it, of which each request of a batch uses its own: y = base(x) + sum_j w_j B_j (A_j x).
 
-    A bf16 [adapters, rank, in_features], B bf16 [adapters, out_features, rank].  Which rows use which adapters is
-    the batch's plan (``set_plan``; rows are counted after flattening the leading dimensions); without a plan
-    the layer is its base.  A compiled layer takes one plan after another without being compiled again: the plan's
-    sizes are data, in a small host tensor (and inductor's CUDA graphs leave the adapters' calls out: the number of
-    blocks launched follows from the sizes).  For inference: a backward pass through the adapters raises.  (The adapters are added to
-    the base's output in place, into a copy only where gradients are on and something carries them.)"""
+    A bf16 [adapters, rank, in_features], B bf16 [adapters, out_features, rank], the features multiples of 64, the
+    rank of 16 and at most 128 (a plan's slots times the rank too).  Which rows use which adapters is the batch's
+    plan (``set_plan``; rows are counted after flattening the leading dimensions); without a plan the layer is its
+    base.  A compiled layer takes one plan after another without being compiled again: the plan's sizes are data,
+    in a small host tensor (and inductor's CUDA graphs leave the adapters' calls out: the number of blocks launched
+    follows from the sizes).  For inference: a backward pass through the adapters raises.  (The adapters are added
+    to the base's output in place, into a copy only where gradients are on and something carries them.)"""
 
     def __init__(self, base: nn.Module, A: torch.Tensor, B: torch.Tensor):
         super().__init__()
@@ -289,6 +290,12 @@ class LoraLinear(nn.Module):
         if k != base.in_features or tuple(B.shape) != (adapters, base.out_features, rank):
             raise ValueError(f"A {tuple(A.shape)} and B {tuple(B.shape)} do not fit a projection from "
                              f"{base.in_features} to {base.out_features}")
+        if base.in_features % 64 or base.out_features % 64:
+            raise ValueError(f"adapters need features in multiples of 64, got {base.in_features} to {base.out_features}")
+        if rank == 0 or rank % 16 or rank > ops.LORA_MAX_RANK:
+            raise ValueError(f"adapters need a rank in multiples of 16 up to {ops.LORA_MAX_RANK}, got {rank}")
+        if A.dtype != torch.bfloat16 or B.dtype != torch.bfloat16:
+            raise ValueError(f"adapters must be bfloat16, got {A.dtype} and {B.dtype}")
         self.base = base
         self.in_features, self.out_features = base.in_features, base.out_features
         self.register_buffer("A", A)
@@ -298,8 +305,8 @@ class LoraLinear(nn.Module):
 
     @classmethod
     def from_adapters(cls, base: nn.Module, adapters: Sequence[Tuple[torch.Tensor, torch.Tensor]]) -> "LoraLinear":
-        """adapters: (A [r, in_features], B [out_features, r]) of any ranks r, padded here with zeros to the
-        largest, rounded up to a multiple of 16."""
+        """adapters: (A [r, in_features], B [out_features, r]) of any ranks r up to 128, padded here with zeros to
+        the largest, rounded up to a multiple of 16."""
         rank = (max(a.shape[0] for a, _ in adapters) + 15) // 16 * 16
         dev = adapters[0][0].device
         A = torch.zeros((len(adapters), rank, base.in_features), dtype=torch.bfloat16, device=dev)
@@ -311,12 +318,22 @@ class LoraLinear(nn.Module):
             B[i, :, : b.shape[1]] = b
         return cls(base, A, B)
 
+    def check_plan(self, plan: ops.LoraPlan) -> None:
+        """Raises where the layer cannot serve the plan."""
+        adapters, rank, _ = self.A.shape
+        if plan.adapters != adapters:
+            raise ValueError(f"the plan is for {plan.adapters} adapters, the layer has {adapters}")
+        if plan.slots * rank > ops.LORA_MAX_RANK:
+            raise ValueError(f"a plan of {plan.slots} slots needs adapters of rank {ops.LORA_MAX_RANK // plan.slots} at "
+                             f"most, the layer's have rank {rank}")
+
     def set_plan(self, plan: Optional[ops.LoraPlan]) -> None:
         if plan is None:
             self.plan_words = self.plan_sizes = None
             return
+        self.check_plan(plan)
         self.plan_words = plan.words
-        self.plan_sizes = torch.tensor(plan.sizes(), dtype=torch.int64)
+        self.plan_sizes = torch.tensor(plan.sizes(), dtype=torch.int64, device="cpu")
         torch._dynamo.maybe_mark_dynamic(self.plan_words, 0)   # plans differ in length
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
@@ -352,10 +369,14 @@ def attach_adapters(model: nn.Module, factory: Callable[[str, nn.Module], Option
 
 
 def set_lora_plan(model: nn.Module, plan: Optional[ops.LoraPlan]) -> None:
-    """Sets the batch's plan (None: no adapters) on every LoraLinear of ``model``."""
-    for m in model.modules():
-        if isinstance(m, LoraLinear):
-            m.set_plan(plan)
+    """Sets the batch's plan (None: no adapters) on every LoraLinear of ``model``; on none where one of them cannot
+    serve it."""
+    layers = [m for m in model.modules() if isinstance(m, LoraLinear)]
+    if plan is not None:
+        for m in layers:
+            m.check_plan(plan)
+    for m in layers:
+        m.set_plan(plan)
 
 
 def swap_linears(model: nn.Module, factory: Callable[[str, nn.Linear], Optional[nn.Module]]) -> int:

@@ -192,3 +192,42 @@ def test_one_compiled_graph_serves_every_plan(host_kernel):
         assert len(sizes) > 15 and len(compiles) == 1
         layer.set_plan(None)
         assert torch.equal(run(x), base(x)) and len(compiles) == 2
+
+
+def test_unsupported_pools_are_refused_when_the_layer_is_built():
+    def build(K, N, rank, dtype=torch.bfloat16):
+        return T.LoraLinear(nn.Linear(K, N), torch.zeros((2, rank, K), dtype=dtype), torch.zeros((2, N, rank), dtype=dtype))
+
+    assert build(64, 64, 128).A.shape == (2, 128, 64)
+    for bad, message in (((96, 64, 16), "multiples of 64"), ((64, 100, 16), "multiples of 64"), ((64, 64, 24), "rank"),
+                         ((64, 64, 144), "rank"), ((64, 64, 0), "rank"), ((64, 64, 16, torch.float32), "bfloat16")):
+        with pytest.raises(ValueError, match=message):
+            build(*bad)
+    with pytest.raises(ValueError, match="rank"):
+        T.LoraLinear.from_adapters(_awq(), _pool(ranks=(4, 129)))
+    assert T.LoraLinear.from_adapters(_awq(), _pool(ranks=(4, 113))).A.shape[1] == 128
+
+
+def test_plans_that_a_layer_cannot_serve_are_refused_when_they_are_set():
+    model = nn.Sequential(T.LoraLinear.from_adapters(_awq(), _pool(ranks=(16, 64))),
+                          T.LoraLinear.from_adapters(_awq(), _pool(ranks=(128, 4))))
+    one = P.LoraPlan([0, 4], [1], [1.0], 4, 2, device="cpu")
+    two = P.LoraPlan([0, 4], [[1, 0]], [[1.0, 1.0]], 4, 2, device="cpu")
+    T.set_lora_plan(model, one)
+    model[0].set_plan(two)
+    model[0].set_plan(one)
+    with pytest.raises(ValueError, match="2 slots needs adapters of rank 64"):
+        T.set_lora_plan(model, two)
+    assert all(m.plan_words is one.words for m in model)        # neither layer took it
+    with pytest.raises(ValueError, match="3 adapters"):
+        model[1].set_plan(P.LoraPlan([0, 4], [1], [1.0], 4, 3, device="cpu"))
+    T.set_lora_plan(model, None)
+    assert all(m.plan_words is None for m in model)
+
+
+def test_a_default_device_does_not_move_the_plans_sizes():
+    base, layer = _linear_layer()
+    plan = P.LoraPlan([0, 4], [1], [1.0], 4, 2, device="cpu")
+    with torch.device("meta"):
+        layer.set_plan(plan)
+    assert layer.plan_sizes.tolist() == plan.sizes()
