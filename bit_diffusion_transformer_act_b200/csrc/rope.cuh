@@ -5,15 +5,18 @@
 // Mathematics.  A head's rotary pairs are dealt to the axes in order (axis a has d_a / 2 pairs);
 // pair i of axis a turns by position[m, a] * theta_a^(-2 i / d_a).  Only the angle's fraction of a
 // turn counts, so the host passes each pair's frequency in turns, f = theta_a^(-2 i / d_a) / (2 pi), and the
-// kernels form the fraction in units of 2^-32 turns:
-//   - integer positions: f as a 64-bit fixed-point fraction; position * f modulo one turn is the
-//     product modulo 2^64, of which the upper half is kept -- exact but for f's own rounding (2^-64);
+// kernels round the fraction to units of 2^-32 turns:
+//   - integer positions: f as a 64-bit fixed-point fraction; position * f modulo one turn is the product modulo
+//     2^64, of which the upper half is kept, rounded (f's own end is off by less than 2^-64 per unit of position);
 //   - float positions: position * f in 64-bit floating point, less the nearest integer.
-// (A product in 32 bits would be off by position * 2^-24 radians: 0.004 at position 65536.)  The fraction's
-// upper two bits, rounded, are the quarter; the rest is an angle within pi / 4, exact to 2^-24 of itself
-// as a float, whose sine and cosine are the Taylor polynomials of degree 9 and 8: their remainders are at
-// most x^11 / 11! < 2^-29 and x^10 / 10! < 2^-25 there.  Thus 28 instructions per pair, where the 64-bit
-// reduction and the library's sine and cosine of any argument took about 100.
+// So the angle is off by half a unit, 2 pi 2^-33 = 7.3e-10 radians (twice that at integer positions near 2^31),
+// whatever its size: of a small angle that is more than 2^-24 of itself, of the rotated values it is far below
+// their last bit.  (A product in 32 bits would be off by position * 2^-24 radians: 0.004 at position 65536.)  The
+// fraction's upper two bits, rounded, are the quarter; the rest is an angle within pi / 4, as a float within
+// 3 * 2^-24 of itself, whose sine and cosine are the Taylor polynomials of degree 9 and 8: their remainders are at
+// most x^11 / 11! < 2^-29 and x^10 / 10! < 2^-25 there.  Sine and cosine come out within 4.5 * 2^-24 of themselves,
+// beside the angle's 7.3e-10.  28 instructions per pair, where the 64-bit reduction and the library's sine and
+// cosine of any argument took about 100.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -75,9 +78,10 @@ __device__ __forceinline__ uint32_t turn_fraction(double pos, uint64_t f) {
 }
 __device__ __forceinline__ uint32_t turn_fraction(int pos, uint64_t f) {
   const uint32_t p = static_cast<uint32_t>(pos), hi = static_cast<uint32_t>(f >> 32), lo = static_cast<uint32_t>(f);
-  // upper half of pos * f modulo 2^64 (pos < 0: its unsigned value less 2^32, whose product with f's low
-  // half comes back off the upper half)
-  return p * hi + __umulhi(p, lo) - (pos < 0 ? lo : 0u);
+  // upper half of pos * f modulo 2^64, rounded (pos < 0: its unsigned value less 2^32, whose product with f's
+  // low half comes back off the upper half)
+  const uint64_t low = static_cast<uint64_t>(p) * lo + 0x80000000u;
+  return p * hi + static_cast<uint32_t>(low >> 32) - (pos < 0 ? lo : 0u);
 }
 
 // Sine and cosine of `frac` * 2^-32 turns; NaN where `bad` is (else it is 0).

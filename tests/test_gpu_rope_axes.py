@@ -218,3 +218,25 @@ def test_axes_given_as_tensors_are_read_at_every_call(P):
     thetas[1].fill_(10.0)
     assert torch.equal(P.svdq_rope_axes_tables(pos, [8, 16], thetas, 32)[0],
                        P.svdq_rope_axes_tables(pos, [8, 16], [100.0, 10.0], 32)[0])
+
+
+@pytest.mark.parametrize("theta,d", [(1e4, 56), (1e6, 64), (1e9, 64), (256.0, 36), (3.0, 2)])
+def test_small_angles_are_rounded_to_the_nearest_unit(P, theta, d):
+    """The angle is rounded to 2^-32 turns (half a unit, 2^-33 turns, and 2^-64 turns per unit of position for the
+    frequency); sine and cosine are off by 4.5 * 2^-24 of themselves -- the reduced angle as a float by three
+    roundings, which reach them with a factor of at most 1, the polynomial's last rounding, and less than half a
+    rounding of its inner terms and its remainder; the float64 angle by a few 2^-53.  Cut off instead of rounded, the
+    angle is off by twice as much, which small angles show."""
+    r = np.random.default_rng(0)
+    near = np.array([0, 1, -1, 2, -2, 3, 17, -200, 96, 1000, 4097, 69999, -69999])
+    pos = np.concatenate([near, r.integers(-200, 70000, 243)])
+    width = (d + 7) // 8 * 8
+    dims, thetas = ([d], [theta]) if width == d else ([d, width - d], [theta, 1e4])
+    both = np.stack([pos] * len(dims), 1)
+    ang = oracle.angles(both, dims, thetas).T
+    for t in (torch.int32, torch.float32):
+        cos, sin = P.svdq_rope_axes_tables(torch.from_numpy(both).to(t).cuda(), dims, thetas, width)
+        for got, exact in ((cos, np.cos(ang)), (sin, np.sin(ang))):
+            tol = 2 * np.pi * (2.0 ** -33 + np.abs(pos) * 2.0 ** -64) + 4.5 * 2.0 ** -24 * np.abs(exact) + \
+                np.abs(ang) * 2.0 ** -50
+            assert (np.abs(_np(got) - exact) <= tol).all()
