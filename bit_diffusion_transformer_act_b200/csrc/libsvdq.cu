@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cstdlib>
 #include <numeric>
 #include <cmath>
 #include <mutex>
@@ -1202,9 +1203,21 @@ static bool heads_distinct(const HeadsView& v, int M, int D) {
   return by_token || by_head || (v.heads == 1 && v.row >= D);
 }
 static bool heads_overlap(const HeadsView& a, const HeadsView& b, int M, int D) {
-  // token-major views are matrices of rows; any other is told apart by its range only
+  // token-major views are matrices of rows
   const int64_t wa = (a.heads - 1) * a.head + D, wb = (b.heads - 1) * b.head + D;
-  return rows_overlap(a.ptr, a.row, wa, b.ptr, b.row, wb, M);
+  if (!rows_overlap(a.ptr, a.row, wa, b.ptr, b.row, wb, M)) return false;
+  // Rows that interlace (q and k of one head side by side) are told apart where the strides are the same:
+  // heads m, h of a and m', h' of b meet where b's start is row (m - m') + head (h - h') from a's to within D.
+  const int64_t head = a.heads > 1 ? a.head : b.head, row = a.row;
+  if ((M > 1 && (row != b.row || row <= 0)) || (b.heads > 1 && b.head != head)) return true;   // others by their range
+  const int64_t delta = (reinterpret_cast<intptr_t>(b.ptr) - reinterpret_cast<intptr_t>(a.ptr)) / 2;
+  for (int64_t dh = 1 - b.heads; dh < a.heads; ++dh) {
+    const int64_t left = delta - head * dh;
+    const int64_t below = M > 1 ? left / row - (left % row < 0) : 0;   // floor
+    for (int64_t dm = below; dm <= below + 1; ++dm)
+      if (dm > -M && dm < M && std::abs(left - row * dm) < D) return true;
+  }
+  return false;
 }
 
 int svdq_qk_norm_rope(const void* Q, int64_t q_row_stride, int64_t q_head_stride, int q_heads, const void* K,

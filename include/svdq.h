@@ -396,7 +396,8 @@ int svdq_lora_add(const void* X, int64_t ldx, const void* Yin, int64_t ldyin, co
  *     be 0 (its pointers are then not used).
  *   norm_wq, norm_wk  device bf16 [head_dim], or NULL: no normalisation of q or k (eps is then not used)
  *   pairing 0: pair i is (x[2 i], x[2 i + 1]) (as svdq_w4a4_nvfp4_linear_qkv); 1: (x[i], x[i + rotated / 2])
- *   out_q may be Q with Q's strides (in place), likewise out_k; an output overlaps nothing else.
+ *   out_q may be Q with Q's strides (in place), likewise out_k; an output overlaps nothing else (heads of
+ *     q and k may lie side by side in a row, as in [M, heads, 3, D]).
  * head_dim % 8 == 0, 8..256; Q, K, the outputs and the norm weights 16-byte aligned, positions 4-byte aligned;
  * q_heads, k_heads <= 65536, and M times the heads below 2^31.
  *

@@ -240,3 +240,17 @@ def test_small_angles_are_rounded_to_the_nearest_unit(P, theta, d):
             tol = 2 * np.pi * (2.0 ** -33 + np.abs(pos) * 2.0 ** -64) + 4.5 * 2.0 ** -24 * np.abs(exact) + \
                 np.abs(ang) * 2.0 ** -50
             assert (np.abs(_np(got) - exact) <= tol).all()
+
+
+@pytest.mark.parametrize("M", [1, 300])
+def test_q_k_and_v_of_a_head_side_by_side(P, M):
+    """[M, heads, 3, D] in place: as from separate tensors, v as it was."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    packed = torch.randn((M, 5, 3, 64), generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randn(64, generator=g, device="cuda").to(torch.bfloat16)
+    pos = _positions(M, 2, False, 4)
+    keep = packed.clone()
+    q, k, v = packed.unbind(2)
+    eq, ek = P.svdq_qk_norm_rope(q.contiguous(), k.contiguous(), w, None, 1e-6, pos, [32, 24], 1e4)
+    P.svdq_qk_norm_rope(q, k, w, None, 1e-6, pos, [32, 24], 1e4, out_q=q, out_k=k)
+    assert torch.equal(q, eq) and torch.equal(k, ek) and torch.equal(v, keep[:, :, 2])

@@ -130,3 +130,45 @@ def test_oracle_is_the_single_axis_oracle_on_one_axis():
     # halves: the same rotation after sorting even before odd columns
     order = np.concatenate([np.arange(0, 16, 2), np.arange(1, 16, 2)])
     assert np.allclose(rope_axes.rotate(x[..., order], ang, half=True), rope_axes.rotate(x, ang, half=False)[..., order])
+
+
+def _elements(base, strides, heads, M, D):
+    at = base + strides[0] * np.arange(M)[:, None] + strides[1] * np.arange(heads)
+    return set((at[..., None] + np.arange(D)).ravel().tolist())
+
+
+@needs_no_device
+def test_heads_of_q_and_k_side_by_side_in_place():
+    """[M, heads, 3, D]: the rows of q and k interlace, which was refused although no element is shared."""
+    s = (2 * 384, 384)
+    assert _rope(q=_at(1), qs=s, k=_at(1, 256), ks=s, oq=_at(1), oqs=s, ok=_at(1, 256), oks=s) == OK
+    one = (5 * 128, 2 * 128)                           # one k head between two of q's
+    assert _rope(q=_at(1), qs=one, k=_at(1, 256), ks=(640, 8), nk=1, oq=_at(1), oqs=one, ok=_at(1, 256), oks=(640, 8)) == OK
+    assert _rope(q=_at(1), qs=one, k=_at(1, 512), ks=(640, 8), nk=1, oq=_at(1), oqs=one, ok=_at(1, 512), oks=(640, 8)) == 1
+    assert _rope(q=_at(1), qs=s, k=_at(1, 240), ks=s, oq=_at(1), oqs=s, ok=_at(1, 240), oks=s) == 1
+
+
+@needs_no_device
+@pytest.mark.parametrize("seed", range(6))
+def test_overlaps_of_equal_strides_are_found_exactly(seed):
+    r = np.random.default_rng(seed)
+    answers = []
+    for _ in range(400):
+        M, nq, nk, D = int(r.integers(1, 5)), int(r.integers(1, 5)), int(r.integers(1, 5)), 8 * int(r.integers(1, 4))
+        head = D + 8 * int(r.integers(0, 6))
+        row = (max(nq, nk) - 1) * head + D + 8 * int(r.integers(0, 8))
+        if r.random() < 0.3:                           # head-major
+            row, head = D + 8 * int(r.integers(0, 4)), 0
+            head = (M - 1) * row + D + 8 * int(r.integers(0, 4))
+        q0 = 1 << 19
+        k0 = q0 + 8 * int(r.integers(-40, 40))
+        apart = not _elements(q0, (row, head), nq, M, D) & _elements(k0, (row, head), nk, M, D)
+        q, k = ctypes.c_void_p(2 * q0), ctypes.c_void_p(2 * k0)
+        st = _rope(q=q, qs=(row, head), nq=nq, k=k, ks=(row, head), nk=nk, M=M, D=D, P_=M, dims=(8,), oq=q,
+                   oqs=(row, head), ok=k, oks=(row, head))
+        if not apart:
+            assert st == 1
+        answers.append((apart, st == OK))
+    wrong = [a for a in answers if a[0] != a[1]]
+    assert not wrong, len(wrong)
+    assert len(set(answers)) == 2
