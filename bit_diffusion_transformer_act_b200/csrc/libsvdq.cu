@@ -1095,7 +1095,7 @@ int svdq_lora_add(const void* X, int64_t ldx, const void* Yin, int64_t ldyin, co
   if (M == 0) return SVDQ_OK;
   if (!Yin || !Y || !aligned16(Yin) || !aligned16(Y) || ldyin < N || ldy < N || ldyin % 8 != 0 || ldy % 8 != 0)
     return SVDQ_ERR_INVALID_ARG;
-  const bool in_place = Y == Yin && ldy == ldyin;
+  const bool in_place = Y == Yin && (ldy == ldyin || M == 1);   // a single row's stride says nothing
   if (!in_place && rows_overlap(Yin, ldyin, N, Y, ldy, N, M)) return SVDQ_ERR_INVALID_ARG;
   if (!plan_dev || !aligned16(plan_dev) || plan_bytes < static_cast<size_t>(plan->bytes)) return SVDQ_ERR_INVALID_ARG;
   const bool work = plan->tiles > 0 || plan->groups > 0;

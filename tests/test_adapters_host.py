@@ -184,3 +184,9 @@ def test_python_wrapper_refuses_before_the_call():
         P.svdq_lora_add(torch.zeros((64, 4), dtype=bf).t(), y, a, b, plan)
     with pytest.raises(ValueError, match="LoraPlan"):
         P.svdq_lora_add(x, y, a, b, None)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-device path")
+def test_a_single_row_is_in_place_whatever_its_strides():
+    s = _pack([0, 1], [0], [1], M=1)[1]
+    assert _add(s, X=ctypes.c_void_p(1 << 24), M=1, ldy=256) == 4
