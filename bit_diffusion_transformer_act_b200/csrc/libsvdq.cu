@@ -205,24 +205,19 @@ bool rows_overlap(const void* a, int64_t lda, int64_t wa, const void* b, int64_t
   return !(d >= wa && d + wb <= lda);
 }
 
-// Launches `kernel` with programmatic dependent launch, in clusters of cluster_y CTAs along y.
+// Launches `kernel` with programmatic dependent launch.
 template <class... KArgs, class... Args>
-bool launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, int smem, int cluster_y, void* stream,
-                const Args&... args) {
+bool launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, int smem, void* stream, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // see grid_dependency_wait
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 1;
-  attr[1].val.clusterDim.y = cluster_y;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster_y > 1 ? 2 : 1;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;   // see grid_dependency_wait
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
     (void)cudaGetLastError();
     return false;
@@ -979,7 +974,7 @@ static int lora_tiles_launch(const LoraCall& c, bool copy) {
                    CU_TENSOR_MAP_SWIZZLE_128B) ||
         !set_smem_once<k13::lora_tile_down_kernel>(227 * 1024, c.dev))
       return SVDQ_ERR_CUDA;
-    if (!launch_pdl(k13::lora_tile_down_kernel, dim3(tiles, p.ks), k13::kThreads, smem, 1, c.stream, tX, tX128, tA,
+    if (!launch_pdl(k13::lora_tile_down_kernel, dim3(tiles, p.ks), k13::kThreads, smem, c.stream, tX, tX128, tA,
                     tYin128, p))
       return SVDQ_ERR_CUDA;
   }
@@ -1012,7 +1007,7 @@ static int lora_tiles_launch(const LoraCall& c, bool copy) {
   if (tiles > 0 && !make_tmap(&tB, c.B, bf, 2, static_cast<uint64_t>(p.adapters) * c.N, c.rank, p.wb, k14::kBN, swizzle(p.wb)))
     return SVDQ_ERR_CUDA;
   if (!set_smem_once<k14::lora_tile_up_kernel>(227 * 1024, c.dev)) return SVDQ_ERR_CUDA;
-  if (!launch_pdl(k14::lora_tile_up_kernel, dim3(std::min(p.items, sms)), k14::kThreads, smem, 1, c.stream, tB, tYin,
+  if (!launch_pdl(k14::lora_tile_up_kernel, dim3(std::min(p.items, sms)), k14::kThreads, smem, c.stream, tB, tYin,
                   tYin128, tY, p))
     return SVDQ_ERR_CUDA;
   return SVDQ_OK;
@@ -1041,7 +1036,7 @@ static int lora_groups_launch(const LoraCall& c, bool copy, float* part) {
   p.ks = 1;
   if (p.ngroups > 0) {
     p.ks = lora_short_splits(p.ngroups, c.K, c.jr, c.dev);
-    if (!launch_pdl(k11::lora_short_down_kernel, dim3(p.ngroups, c.jr / 16, p.ks), k11::kThreads, 0, 1, c.stream, p))
+    if (!launch_pdl(k11::lora_short_down_kernel, dim3(p.ngroups, c.jr / 16, p.ks), k11::kThreads, 0, c.stream, p))
       return SVDQ_ERR_CUDA;
   }
   const int all = p.ngroups + (copy ? c.plan->copy_groups : 0);
@@ -1055,7 +1050,7 @@ static int lora_groups_launch(const LoraCall& c, bool copy, float* part) {
   case STEPS_:                                                                                                       \
     return set_smem_once<k11::lora_short_up_kernel<WIDE_, STEPS_>>(                                                  \
                std::max(k11::kUpRingBytes, 2 * k11::kUpWarps * k11::up_piece_bytes(svdq::kLoraMaxRank)), c.dev) &&  \
-                   launch_pdl(k11::lora_short_up_kernel<WIDE_, STEPS_>, grid, k11::kUpThreads, smem, 1, c.stream, p) \
+                   launch_pdl(k11::lora_short_up_kernel<WIDE_, STEPS_>, grid, k11::kUpThreads, smem, c.stream, p) \
                ? SVDQ_OK                                                                                             \
                : SVDQ_ERR_CUDA
   if (c.rank % 32 == 0) {
@@ -1299,7 +1294,7 @@ int svdq_qk_norm_rope(const void* Q, int64_t q_row_stride, int64_t q_head_stride
   const int kind = (pairing ? 2 : 0) + (positions_float ? 1 : 0);
 #define SVDQ_ROPE_LAUNCH(V_, L_, H_, F_)                                                               \
   (set_smem_once<k9::qk_norm_rope_kernel<V_, L_, H_, F_>>(k9::kRingBytes + k9::kAfterBytes, dev) &&         \
-           launch_pdl(k9::qk_norm_rope_kernel<V_, L_, H_, F_>, grid, k9::kThreads, smem, 1, stream, p, fr) \
+           launch_pdl(k9::qk_norm_rope_kernel<V_, L_, H_, F_>, grid, k9::kThreads, smem, stream, p, fr) \
        ? launch_status()                                                                                  \
        : SVDQ_ERR_CUDA)
 #define SVDQ_ROPE_CASE(V_, L_)                                                                            \
@@ -1349,7 +1344,7 @@ int svdq_rope_axes_tables(const void* positions, int positions_float, int P, int
   // pairs per thread: the fewest that keep the grid within eight blocks per SM
   const int by = std::max(1, std::min(p.pairs, 8 * sm_count(dev) / bx));
   p.per = (p.pairs + by - 1) / by;
-  if (!launch_pdl(positions_float ? k9::rope_tables_kernel<true> : k9::rope_tables_kernel<false>, dim3(bx, (p.pairs + p.per - 1) / p.per), k9::kTableThreads, 0, 1, stream, p, fr))
+  if (!launch_pdl(positions_float ? k9::rope_tables_kernel<true> : k9::rope_tables_kernel<false>, dim3(bx, (p.pairs + p.per - 1) / p.per), k9::kTableThreads, 0, stream, p, fr))
     return SVDQ_ERR_CUDA;
   return launch_status();
 }

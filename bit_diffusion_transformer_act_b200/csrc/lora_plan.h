@@ -4,7 +4,8 @@
 //   [0, 16)   header: "SVDQLORA", M, requests, slots, adapters, tiles, copy_tiles, groups, copy_groups
 //   tiles     [tiles + copy_tiles][tile words]   rows of one long request: {first row, rows (1..128),
 //             request, 0}, its ids [slots] and its weights [slots] (float bits); the copy tiles cover
-//             runs of rows that no adapter touches (request -1)
+//             runs of rows that no adapter touches (request -1; no kernel reads the request, it says whose
+//             rows they are to who looks at a plan)
 //   groups    [groups + copy_groups][group words]   rows of short requests with the same adapters,
 //             gathered: {rows (1..16), 0, 0, 0}, ids [8], row indexes [16], weights [16][slots]; the
 //             copy groups hold the rows of short untouched runs (every id -1) of a plan without tiles
