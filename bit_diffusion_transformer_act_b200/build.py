@@ -13,7 +13,8 @@ LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libsvdq.so")
 SOURCES = ["libsvdq.cu", "host_pack.cpp", "host_lora.cpp"]
 DEPS = SOURCES + ["ptx.cuh", "quant_act.cuh", "gemm_nvfp4.cuh", "awq_w4a16.cuh", "awq_umma.cuh", "act_amax.cuh", "layout.h",
-                  "nvfp4_quant.cuh", "gemm_gelu_quant.cuh", "gemm_int4.cuh", "lora_plan.h", "lora_short.cuh", "lora_tile.cuh", "rope.cuh",
+                  "nvfp4_quant.cuh", "gemm_gelu_quant.cuh", "gemm_int4.cuh", "lora_plan.h", "lora_short.cuh", "lora_tile.cuh", "lora_launch.cuh",
+                  "rope.cuh", "rope_launch.cuh",
                   os.path.join("..", "..", "include", "svdq.h")]
 
 NVCC_FLAGS = [

@@ -5,11 +5,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <string.h>
-
 #include <algorithm>
 #include <atomic>
-#include <cstdlib>
 #include <numeric>
 #include <cmath>
 #include <mutex>
@@ -25,9 +22,6 @@
 #include "awq_umma.cuh"
 #include "gemm_gelu_quant.cuh"
 #include "gemm_int4.cuh"
-#include "lora_short.cuh"
-#include "lora_tile.cuh"
-#include "rope.cuh"
 
 // Scratch of svdq_act_amax_noalloc: kernel 5's result word, partial maximum and block
 // counter, for callers that cannot allocate device memory.  Every GPU that loads this
@@ -193,36 +187,6 @@ int amax_noalloc_scratch(int dev, unsigned int** out) {
   }
   *out = reinterpret_cast<unsigned int*>(a);
   return SVDQ_OK;
-}
-
-// Two row-strided bf16 matrices (elements (m, c) at ptr[m * ld + c], c < width): whether they may share an
-// element.  Windows of one matrix (equal row strides) are told apart by their columns.
-bool rows_overlap(const void* a, int64_t lda, int64_t wa, const void* b, int64_t ldb, int64_t wb, int64_t rows) {
-  const intptr_t pa = reinterpret_cast<intptr_t>(a) / 2, pb = reinterpret_cast<intptr_t>(b) / 2;
-  if (pa + (rows - 1) * lda + wa <= pb || pb + (rows - 1) * ldb + wb <= pa) return false;
-  if (lda != ldb || wa > lda || wb > lda) return true;
-  const int64_t d = ((pb - pa) % lda + lda) % lda;        // b's first column in a's rows
-  return !(d >= wa && d + wb <= lda);
-}
-
-// Launches `kernel` with programmatic dependent launch.
-template <class... KArgs, class... Args>
-bool launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, int smem, void* stream, const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;   // see grid_dependency_wait
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return false;
-  }
-  return true;
 }
 
 int launch_status() {
@@ -881,474 +845,6 @@ int awq_w4a16_linear(const void* X, const void* qweight, const void* scales, con
   return launch_status();
 }
 
-// CTAs over which a group's K is split in kernel 11: as many as keep the grid within about four CTAs
-// per SM, each with at least 16 steps of 32 K (two per warp).
-static int lora_short_splits(int groups, int K, int jr, int dev) {
-  const int64_t ctas = static_cast<int64_t>(groups) * (jr / 16);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({4 * sm_count(dev) / ctas, K / 512, 16})));
-}
-
-static bool lora_plan_ok(const svdq_lora_plan* p) {
-  return p && p->M >= 0 && p->requests >= 0 && p->slots >= 1 && p->slots <= svdq::kLoraMaxSlots && p->adapters >= 0 &&
-         p->tiles >= 0 && p->copy_tiles >= 0 && p->groups >= 0 && p->copy_groups >= 0 &&
-         p->bytes == static_cast<int64_t>(4 * svdq::lora_layout(p->slots, static_cast<size_t>(p->tiles) + p->copy_tiles,
-                                                                static_cast<size_t>(p->groups) + p->copy_groups).words);
-}
-
-// Slices of K in kernel 13: as many as keep the grid within one CTA per SM (its ring then takes all of the
-// shared memory), at least one, at most the 64-column chunks of K and four (kernel 14 reads every part).
-// 4608 x 2560 -> 7680, 64 ranks, both kernels: 45.6, 39.3, 38.2, 38.8, 42.4, 44.2 us with 1, 2, 3, 4, 6, 8
-// slices; 9001 x 10240 -> 2560, 128 ranks: 92, 69, 82, 77 us with 1, 2, 3, 4 (two is one CTA per SM).
-static int lora_tile_splits(int tiles, int K, int dev) {
-  return std::max(1, std::min({sm_count(dev) / std::max(1, tiles), K / 64, 4}));
-}
-
-// The workspace: kernel 13's parts, then kernel 11's.
-struct LoraWorkspace {
-  size_t part, total;
-};
-static LoraWorkspace lora_workspace(const svdq_lora_plan* p, int K, int jr, int dev) {
-  LoraWorkspace w;
-  w.part = static_cast<size_t>(p->tiles) * lora_tile_splits(p->tiles, K, dev) * svdq::kLoraTileRows * jr * sizeof(float);
-  w.total = w.part;
-  if (p->groups > 0)
-    w.total += static_cast<size_t>(p->groups) * lora_short_splits(p->groups, K, jr, dev) * svdq::kLoraGroupRows * jr *
-               sizeof(float);
-  w.total = std::max<size_t>(w.total, 16);
-  return w;
-}
-
-size_t svdq_lora_workspace_bytes(const svdq_lora_plan* plan, int K, int rank) {
-  if (!lora_plan_ok(plan) || K <= 0 || K % 64 != 0 || rank <= 0 || rank % 16 != 0 ||
-      plan->slots * static_cast<int64_t>(rank) > svdq::kLoraMaxRank)
-    return 0;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
-    (void)cudaGetLastError();
-    return 0;
-  }
-  return lora_workspace(plan, K, plan->slots * rank, dev).total;
-}
-
-// One call's arguments, checked.
-struct LoraCall {
-  const void *X, *Yin, *A, *B;
-  void *Y, *ws, *stream;
-  int64_t ldx, ldyin, ldy;
-  const svdq_lora_plan* plan;
-  const int32_t *tiles, *groups;                    // the plan's sections on the device
-  int M, N, K, rank, jr, dev;
-};
-
-// Kernels 13 and 14: the tiles of long requests, and (copy) of the rows to copy.
-static int lora_tiles_launch(const LoraCall& c, bool copy) {
-  namespace k13 = svdq::k13;
-  namespace k14 = svdq::k14;
-  const int tiles = c.plan->tiles, all = tiles + (copy ? c.plan->copy_tiles : 0);
-  const int jr = c.jr;
-  const int sms = sm_count(c.dev);
-  const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  if (tiles > 0) {
-    k13::Params p;
-    p.tiles = c.tiles;
-    p.parts = static_cast<float*>(c.ws);
-    p.K = c.K;
-    p.rank = c.rank;
-    p.slots = c.plan->slots;
-    p.adapters = c.plan->adapters;
-    p.ks = lora_tile_splits(tiles, c.K, c.dev);
-    // one CTA per SM takes all of the shared memory, a larger grid leaves room for three
-    const int room = static_cast<int64_t>(tiles) * p.ks <= sms ? 227 * 1024 : 75 * 1024;
-    p.stages = std::min(k13::kMaxStages, (room - k13::kSmemExtra) / k13::stage_bytes(jr));
-    const int smem = p.stages * k13::stage_bytes(jr) + k13::kSmemExtra;
-    p.N = c.N;
-    p.up_chunks = (c.N + k14::kBN - 1) / k14::kBN;
-    p.up_items = all * p.up_chunks;
-    p.up_ctas = std::min(p.up_items, sms);
-    p.up_ahead = std::min(k13::kYAhead, p.up_items / sms);
-    CUtensorMap tX, tX128, tA, tYin128;
-    if (!make_tmap(&tX, c.X, bf, 2, c.M, c.K, k13::kChunk, 32, CU_TENSOR_MAP_SWIZZLE_128B, c.ldx) ||
-        !make_tmap(&tX128, c.X, bf, 2, c.M, c.K, k13::kChunk, 128, CU_TENSOR_MAP_SWIZZLE_128B, c.ldx) ||
-        !make_tmap(&tYin128, c.Yin, bf, 2, c.M, c.N, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, c.ldyin) ||
-        !make_tmap(&tA, c.A, bf, 2, static_cast<uint64_t>(p.adapters) * c.rank, c.K, k13::kChunk, c.rank,
-                   CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !set_smem_once<k13::lora_tile_down_kernel>(227 * 1024, c.dev))
-      return SVDQ_ERR_CUDA;
-    if (!launch_pdl(k13::lora_tile_down_kernel, dim3(tiles, p.ks), k13::kThreads, smem, c.stream, tX, tX128, tA,
-                    tYin128, p))
-      return SVDQ_ERR_CUDA;
-  }
-  k14::Params p;
-  p.tiles = c.tiles;
-  p.parts = static_cast<const float*>(c.ws);
-  p.ks = lora_tile_splits(tiles, c.K, c.dev);
-  p.Y = static_cast<__nv_bfloat16*>(c.Y);
-  p.ldy = c.ldy;
-  p.ntiles = tiles;
-  p.N = c.N;
-  p.chunks = (c.N + k14::kBN - 1) / k14::kBN;
-  p.items = all * p.chunks;
-  p.rank = c.rank;
-  p.slots = c.plan->slots;
-  p.adapters = c.plan->adapters;
-  p.wb = c.rank % 64 == 0 ? 64 : c.rank % 32 == 0 ? 32 : 16;
-  p.early = tiles > 0;
-  p.stages = std::min(k14::kMaxStages, (227 * 1024 - k14::kSmemExtra) / k14::stage_bytes(jr));
-  const int smem = p.stages * k14::stage_bytes(jr) + k14::kSmemExtra;
-  auto swizzle = [](int w) {
-    return w == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : w == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
-  };
-  CUtensorMap tB, tYin, tYin128, tY;
-  if (!make_tmap(&tYin, c.Yin, bf, 2, c.M, c.N, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B, c.ldyin) ||
-      !make_tmap(&tYin128, c.Yin, bf, 2, c.M, c.N, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, c.ldyin) ||
-      !make_tmap(&tY, c.Y, bf, 2, c.M, c.N, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B, c.ldy))
-    return SVDQ_ERR_CUDA;
-  tB = tY;                                          // not read when every tile is a copy
-  if (tiles > 0 && !make_tmap(&tB, c.B, bf, 2, static_cast<uint64_t>(p.adapters) * c.N, c.rank, p.wb, k14::kBN, swizzle(p.wb)))
-    return SVDQ_ERR_CUDA;
-  if (!set_smem_once<k14::lora_tile_up_kernel>(227 * 1024, c.dev)) return SVDQ_ERR_CUDA;
-  if (!launch_pdl(k14::lora_tile_up_kernel, dim3(std::min(p.items, sms)), k14::kThreads, smem, c.stream, tB, tYin,
-                  tYin128, tY, p))
-    return SVDQ_ERR_CUDA;
-  return SVDQ_OK;
-}
-
-// Kernels 11 and 12: the groups of short requests, and (copy) of the rows to copy.
-static int lora_groups_launch(const LoraCall& c, bool copy, float* part) {
-  namespace k11 = svdq::k11;
-  k11::Params p;
-  p.X = static_cast<const __nv_bfloat16*>(c.X);
-  p.A = static_cast<const __nv_bfloat16*>(c.A);
-  p.B = static_cast<const __nv_bfloat16*>(c.B);
-  p.Yin = static_cast<const __nv_bfloat16*>(c.Yin);
-  p.Y = static_cast<__nv_bfloat16*>(c.Y);
-  p.ldx = c.ldx;
-  p.ldyin = c.ldyin;
-  p.ldy = c.ldy;
-  p.groups = c.groups;
-  p.part = part;
-  p.N = c.N;
-  p.K = c.K;
-  p.rank = c.rank;
-  p.slots = c.plan->slots;
-  p.ngroups = c.plan->groups;
-  p.early = p.ngroups > 0;
-  p.ks = 1;
-  if (p.ngroups > 0) {
-    p.ks = lora_short_splits(p.ngroups, c.K, c.jr, c.dev);
-    if (!launch_pdl(k11::lora_short_down_kernel, dim3(p.ngroups, c.jr / 16, p.ks), k11::kThreads, 0, c.stream, p))
-      return SVDQ_ERR_CUDA;
-  }
-  const int all = p.ngroups + (copy ? c.plan->copy_groups : 0);
-  const int strips = (c.N / k11::kUpCols + k11::kUpWarps - 1) / k11::kUpWarps;
-  const dim3 grid(all, std::max(1, std::min(strips, 4 * sm_count(c.dev) / all)));   // four CTAs per SM
-  const int passes = (strips - 1) / static_cast<int>(grid.y) + 1;
-  const int piece = k11::kUpWarps * k11::up_piece_bytes(c.jr);   // of all warps of a CTA
-  p.depth = std::max(2, std::min({k11::kUpMaxDepth, k11::kUpRingBytes / piece, passes}));
-  const int smem = p.depth * piece;
-#define SVDQ_LORA_UP(WIDE_, STEPS_)                                                                                  \
-  case STEPS_:                                                                                                       \
-    return set_smem_once<k11::lora_short_up_kernel<WIDE_, STEPS_>>(                                                  \
-               std::max(k11::kUpRingBytes, 2 * k11::kUpWarps * k11::up_piece_bytes(svdq::kLoraMaxRank)), c.dev) &&  \
-                   launch_pdl(k11::lora_short_up_kernel<WIDE_, STEPS_>, grid, k11::kUpThreads, smem, c.stream, p) \
-               ? SVDQ_OK                                                                                             \
-               : SVDQ_ERR_CUDA
-  if (c.rank % 32 == 0) {
-    switch (c.jr / 32) {
-      SVDQ_LORA_UP(true, 1);
-      SVDQ_LORA_UP(true, 2);
-      SVDQ_LORA_UP(true, 3);
-      SVDQ_LORA_UP(true, 4);
-    }
-  } else {
-    switch (c.jr / 16) {
-      SVDQ_LORA_UP(false, 1);
-      SVDQ_LORA_UP(false, 2);
-      SVDQ_LORA_UP(false, 3);
-      SVDQ_LORA_UP(false, 4);
-      SVDQ_LORA_UP(false, 5);
-      SVDQ_LORA_UP(false, 6);
-      SVDQ_LORA_UP(false, 7);
-      SVDQ_LORA_UP(false, 8);
-    }
-  }
-#undef SVDQ_LORA_UP
-  return SVDQ_ERR_UNSUPPORTED_SHAPE;
-}
-
-int svdq_lora_add(const void* X, int64_t ldx, const void* Yin, int64_t ldyin, const void* A, const void* B,
-                  const svdq_lora_plan* plan, const void* plan_dev, size_t plan_bytes, int M, int N, int K, int rank,
-                  void* workspace, size_t workspace_bytes, void* Y, int64_t ldy, void* stream) {
-  if (M < 0 || N <= 0 || K <= 0 || rank <= 0 || !lora_plan_ok(plan) || plan->M != M) return SVDQ_ERR_INVALID_ARG;
-  if (rank % 16 != 0 || plan->slots * static_cast<int64_t>(rank) > svdq::kLoraMaxRank || K % 64 != 0 || N % 64 != 0)
-    return SVDQ_ERR_UNSUPPORTED_SHAPE;
-  // tile coordinates and piece counts are 32-bit
-  const int64_t all_tiles = static_cast<int64_t>(plan->tiles) + plan->copy_tiles;
-  if (static_cast<int64_t>(plan->adapters) * N > INT32_MAX - N || all_tiles * (N / 64) > INT32_MAX ||
-      all_tiles * svdq::kLoraTileRows > INT32_MAX)
-    return SVDQ_ERR_UNSUPPORTED_SHAPE;
-  if (M == 0) return SVDQ_OK;
-  if (!Yin || !Y || !aligned16(Yin) || !aligned16(Y) || ldyin < N || ldy < N || ldyin % 8 != 0 || ldy % 8 != 0)
-    return SVDQ_ERR_INVALID_ARG;
-  const bool in_place = Y == Yin && (ldy == ldyin || M == 1);   // a single row's stride says nothing
-  if (!in_place && rows_overlap(Yin, ldyin, N, Y, ldy, N, M)) return SVDQ_ERR_INVALID_ARG;
-  if (!plan_dev || !aligned16(plan_dev) || plan_bytes < static_cast<size_t>(plan->bytes)) return SVDQ_ERR_INVALID_ARG;
-  const bool work = plan->tiles > 0 || plan->groups > 0;
-  if (work) {
-    if (!X || !A || !B || !workspace || !aligned16(X) || !aligned16(A) || !aligned16(B) || !aligned16(workspace) ||
-        ldx < K || ldx % 8 != 0)
-      return SVDQ_ERR_INVALID_ARG;
-    if (rows_overlap(X, ldx, K, Y, ldy, N, M)) return SVDQ_ERR_INVALID_ARG;
-  }
-  int dev;
-  if (int st = current_device_ok(&dev)) return st;
-  const LoraWorkspace ws = lora_workspace(plan, K, plan->slots * rank, dev);
-  if (work && workspace_bytes < ws.total) return SVDQ_ERR_INVALID_ARG;
-
-  const svdq::LoraLayout L = svdq::lora_layout(plan->slots, all_tiles, static_cast<size_t>(plan->groups) + plan->copy_groups);
-  const int32_t* words = static_cast<const int32_t*>(plan_dev);
-  const LoraCall c{X,    Yin, A, B, Y, workspace, stream, ldx, ldyin, ldy, plan, words + L.tiles, words + L.groups, M, N, K,
-                   rank, plan->slots * rank, dev};
-  if (plan->tiles > 0 || (plan->copy_tiles > 0 && !in_place))
-    if (int st = lora_tiles_launch(c, !in_place)) return st;
-  if (plan->groups > 0 || (plan->copy_groups > 0 && !in_place))
-    if (int st = lora_groups_launch(c, !in_place, reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ws.part)))
-      return st;
-  return launch_status();
-}
-
-// The pairs' frequencies in turns per unit of position, as the kernels read them (see Freqs).  Along an axis they
-// are a geometric sequence, formed in extended precision (128 products of 2^-64 each).  They follow from the
-// axes alone, and a model has one set: the last one of the thread is kept with what it was formed from
-// (forming it costs as much as a launch).
-struct RopeFreqs {
-  int axes = 0, is_float = 0, rot = 0;
-  int32_t dims[svdq::k9::kMaxAxes];
-  double theta[svdq::k9::kMaxAxes];
-  svdq::k9::Freqs fr;
-};
-static const RopeFreqs& rope_freqs(int axes, const int32_t* dims, const double* theta, bool is_float) {
-  static thread_local RopeFreqs r;
-  if (r.axes == axes && r.is_float == is_float && memcmp(r.dims, dims, axes * sizeof(int32_t)) == 0 &&
-      memcmp(r.theta, theta, axes * sizeof(double)) == 0)
-    return r;
-  r.axes = axes;
-  r.is_float = is_float;
-  memcpy(r.dims, dims, axes * sizeof(int32_t));
-  memcpy(r.theta, theta, axes * sizeof(double));
-  int at = 0;
-  for (int a = 0; a < axes; ++a) {
-    const long double ratio = std::pow(static_cast<long double>(theta[a]), -2.0L / dims[a]);
-    long double f = 0.159154943091895335768883763372514362L;   // 1 / (2 pi)
-    for (int i = 0; i < dims[a] / 2; ++i, ++at) {
-      if (is_float) {
-        const double d = static_cast<double>(f);
-        memcpy(&r.fr.f[at], &d, sizeof(d));
-      } else {
-        r.fr.f[at] = static_cast<uint64_t>(std::ldexp(f - std::floor(f), 64));   // whole turns do not count
-      }
-      r.fr.axis[at] = static_cast<uint8_t>(a);
-      f *= ratio;
-    }
-  }
-  r.rot = 2 * at;
-  for (; at < svdq::k9::kMaxPairs; ++at) {
-    r.fr.f[at] = 0;
-    r.fr.axis[at] = 0;
-  }
-  return r;
-}
-
-// Checks of the arguments that both rotary calls share.
-static int rope_check(const void* positions, int P, int axes, const int32_t* dims, const double* theta, int M,
-                      int head_dim) {
-  if (M < 0 || head_dim <= 0 || axes <= 0 || !dims || !theta) return SVDQ_ERR_INVALID_ARG;
-  if (axes > svdq::k9::kMaxAxes || head_dim > 2 * svdq::k9::kMaxPairs) return SVDQ_ERR_UNSUPPORTED_SHAPE;
-  int64_t rot = 0;
-  for (int a = 0; a < axes; ++a) {
-    if (dims[a] <= 0 || !(theta[a] > 0.0) || !std::isfinite(theta[a])) return SVDQ_ERR_INVALID_ARG;
-    if (dims[a] % 2 != 0) return SVDQ_ERR_UNSUPPORTED_SHAPE;
-    rot += dims[a];
-  }
-  if (rot % 8 != 0 || rot > head_dim) return SVDQ_ERR_UNSUPPORTED_SHAPE;
-  if (M == 0) return SVDQ_OK;
-  if (P <= 0 || M % P != 0) return SVDQ_ERR_INVALID_ARG;
-  if (!positions || (reinterpret_cast<uintptr_t>(positions) & 3u)) return SVDQ_ERR_INVALID_ARG;
-  return SVDQ_OK;
-}
-
-// A [M, heads, D] view with strides, made canonical where an extent is 1 (its stride then says nothing).
-struct HeadsView {
-  const void* ptr;
-  int64_t row, head;
-  int heads;
-};
-static HeadsView heads_view(const void* ptr, int64_t row, int64_t head, int heads, int M, int D) {
-  if (heads <= 1) head = D;
-  if (M <= 1) row = std::max<int64_t>(D, head * std::max(1, heads - 1) + D);
-  return {ptr, row, head, heads};
-}
-static bool heads_ok(const HeadsView& v) {
-  return v.ptr && aligned16(v.ptr) && v.row >= 0 && v.head >= 0 && v.row % 8 == 0 && v.head % 8 == 0;
-}
-// No two elements of the view are the same word.
-static bool heads_distinct(const HeadsView& v, int M, int D) {
-  const bool by_token = v.head >= D && v.row >= (v.heads - 1) * v.head + D;
-  const bool by_head = v.row >= D && v.head >= (M - 1) * v.row + D;
-  return by_token || by_head || (v.heads == 1 && v.row >= D);
-}
-static bool heads_overlap(const HeadsView& a, const HeadsView& b, int M, int D) {
-  // token-major views are matrices of rows
-  const int64_t wa = (a.heads - 1) * a.head + D, wb = (b.heads - 1) * b.head + D;
-  if (!rows_overlap(a.ptr, a.row, wa, b.ptr, b.row, wb, M)) return false;
-  // Rows that interlace (q and k of one head side by side) are told apart where the strides are the same:
-  // heads m, h of a and m', h' of b meet where b's start is row (m - m') + head (h - h') from a's to within D.
-  const int64_t head = a.heads > 1 ? a.head : b.head, row = a.row;
-  if ((M > 1 && (row != b.row || row <= 0)) || (b.heads > 1 && b.head != head)) return true;   // others by their range
-  const int64_t delta = (reinterpret_cast<intptr_t>(b.ptr) - reinterpret_cast<intptr_t>(a.ptr)) / 2;
-  for (int64_t dh = 1 - b.heads; dh < a.heads; ++dh) {
-    const int64_t left = delta - head * dh;
-    const int64_t below = M > 1 ? left / row - (left % row < 0) : 0;   // floor
-    for (int64_t dm = below; dm <= below + 1; ++dm)
-      if (dm > -M && dm < M && std::abs(left - row * dm) < D) return true;
-  }
-  return false;
-}
-
-int svdq_qk_norm_rope(const void* Q, int64_t q_row_stride, int64_t q_head_stride, int q_heads, const void* K,
-                      int64_t k_row_stride, int64_t k_head_stride, int k_heads, int M, int head_dim,
-                      const void* norm_wq, const void* norm_wk, float eps, const void* positions, int positions_float,
-                      int P, int axes, const int32_t* axis_dims, const double* axis_theta, int pairing, void* out_q,
-                      int64_t oq_row_stride, int64_t oq_head_stride, void* out_k, int64_t ok_row_stride,
-                      int64_t ok_head_stride, void* stream) {
-  if (q_heads < 0 || k_heads < 0 || q_heads > (1 << 16) || k_heads > (1 << 16) || (pairing != 0 && pairing != 1))
-    return SVDQ_ERR_INVALID_ARG;
-  if ((norm_wq || norm_wk) && (!(eps >= 0.f) || !std::isfinite(eps))) return SVDQ_ERR_INVALID_ARG;
-  if (int st = rope_check(positions, P, axes, axis_dims, axis_theta, M, head_dim)) return st;
-  const int D = head_dim;
-  if (D % 8 != 0) return SVDQ_ERR_UNSUPPORTED_SHAPE;
-  if (M == 0 || q_heads + k_heads == 0) return SVDQ_OK;
-  if ((norm_wq && !aligned16(norm_wq)) || (norm_wk && !aligned16(norm_wk))) return SVDQ_ERR_INVALID_ARG;
-  const HeadsView q = heads_view(Q, q_row_stride, q_head_stride, q_heads, M, D);
-  const HeadsView k = heads_view(K, k_row_stride, k_head_stride, k_heads, M, D);
-  const HeadsView oq = heads_view(out_q, oq_row_stride, oq_head_stride, q_heads, M, D);
-  const HeadsView ok = heads_view(out_k, ok_row_stride, ok_head_stride, k_heads, M, D);
-  auto same = [](const HeadsView& a, const HeadsView& b) { return a.ptr == b.ptr && a.row == b.row && a.head == b.head; };
-  if (q_heads > 0 && (!heads_ok(q) || !heads_ok(oq) || !heads_distinct(oq, M, D) ||
-                      (!same(q, oq) && heads_overlap(q, oq, M, D))))
-    return SVDQ_ERR_INVALID_ARG;
-  if (k_heads > 0 && (!heads_ok(k) || !heads_ok(ok) || !heads_distinct(ok, M, D) ||
-                      (!same(k, ok) && heads_overlap(k, ok, M, D))))
-    return SVDQ_ERR_INVALID_ARG;
-  if (q_heads > 0 && k_heads > 0 &&
-      (heads_overlap(oq, ok, M, D) || heads_overlap(oq, k, M, D) || heads_overlap(ok, q, M, D)))
-    return SVDQ_ERR_INVALID_ARG;
-  int dev;
-  if (int st = current_device_ok(&dev)) return st;
-
-  namespace k9 = svdq::k9;
-  const RopeFreqs& rf = rope_freqs(axes, axis_dims, axis_theta, positions_float != 0);
-  const k9::Freqs& fr = rf.fr;
-  k9::Params p;
-  p.rot = rf.rot;
-  auto view = [](const HeadsView& v) {
-    return k9::View{static_cast<__nv_bfloat16*>(const_cast<void*>(v.ptr)), v.row, v.head};
-  };
-  p.q = view(q);
-  p.k = view(k);
-  p.oq = view(oq);
-  p.ok = view(ok);
-  p.wq = static_cast<const __nv_bfloat16*>(norm_wq);
-  p.wk = static_cast<const __nv_bfloat16*>(norm_wk);
-  p.pos = positions;
-  p.axes = axes;
-  p.P = P;
-  p.M = M;
-  p.q_heads = q_heads;
-  p.k_heads = k_heads;
-  p.D = D;
-  p.eps = eps;
-  // 8 pairs per lane where runs of 8 fit the head and the rotated columns, else 4
-  const int V = D % 16 == 0 && p.rot % 16 == 0 ? 8 : 4;
-  int lpr = 1;
-  while (lpr * 2 * V < D) lpr *= 2;
-  // Groups of heads (what a warp holds at once) per unit: all of a token's, fewer where a unit would exceed
-  // kUnitBytes (so that every warp has two stages), and fewer while there are less than two units for every warp
-  // of the device.
-  const int hpw = 32 / lpr;
-  p.q_groups = (q_heads + hpw - 1) / hpw;
-  p.groups = p.q_groups + (k_heads + hpw - 1) / hpw;
-  const int group_bytes = hpw * D * 2;               // at most 1 KB
-  const int64_t warps = static_cast<int64_t>(k9::kBlocksPerSm) * sm_count(dev) * k9::kWarps;
-  const int64_t least = std::max<int64_t>((p.groups + k9::kUnitBytes / group_bytes - 1) / (k9::kUnitBytes / group_bytes),
-                                          std::min<int64_t>(p.groups, 2 * warps / M));
-  p.chunk = static_cast<int>((p.groups + least - 1) / std::max<int64_t>(1, least));
-  p.units = static_cast<uint32_t>((p.groups + p.chunk - 1) / p.chunk);
-  if (static_cast<int64_t>(M) * p.units > INT32_MAX) return SVDQ_ERR_UNSUPPORTED_SHAPE;
-  p.stage_bytes = (p.chunk * group_bytes + 127) / 128 * 128;
-  p.stage_log = 4;
-  static_assert(2 * k9::kWarps == 1 << 4, "the least stage_log");
-  while ((2 << p.stage_log) <= k9::kMaxStages && (2 << p.stage_log) * p.stage_bytes <= k9::kRingBytes) ++p.stage_log;
-  const int smem = (p.stage_bytes << p.stage_log) + k9::kAfterBytes;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(M) * p.units, static_cast<int64_t>(k9::kBlocksPerSm) * sm_count(dev))));
-  const int kind = (pairing ? 2 : 0) + (positions_float ? 1 : 0);
-#define SVDQ_ROPE_LAUNCH(V_, L_, H_, F_)                                                               \
-  (set_smem_once<k9::qk_norm_rope_kernel<V_, L_, H_, F_>>(k9::kRingBytes + k9::kAfterBytes, dev) &&         \
-           launch_pdl(k9::qk_norm_rope_kernel<V_, L_, H_, F_>, grid, k9::kThreads, smem, stream, p, fr) \
-       ? launch_status()                                                                                  \
-       : SVDQ_ERR_CUDA)
-#define SVDQ_ROPE_CASE(V_, L_)                                                                            \
-  if (V == V_ && lpr == L_)                                                                               \
-    return kind == 0   ? SVDQ_ROPE_LAUNCH(V_, L_, false, false)                                           \
-           : kind == 1 ? SVDQ_ROPE_LAUNCH(V_, L_, false, true)                                            \
-           : kind == 2 ? SVDQ_ROPE_LAUNCH(V_, L_, true, false)                                            \
-                       : SVDQ_ROPE_LAUNCH(V_, L_, true, true)
-  SVDQ_ROPE_CASE(8, 1);
-  SVDQ_ROPE_CASE(8, 2);
-  SVDQ_ROPE_CASE(8, 4);
-  SVDQ_ROPE_CASE(8, 8);
-  SVDQ_ROPE_CASE(8, 16);
-  SVDQ_ROPE_CASE(4, 1);
-  SVDQ_ROPE_CASE(4, 2);
-  SVDQ_ROPE_CASE(4, 4);
-  SVDQ_ROPE_CASE(4, 8);
-  SVDQ_ROPE_CASE(4, 16);
-  SVDQ_ROPE_CASE(4, 32);
-#undef SVDQ_ROPE_CASE
-#undef SVDQ_ROPE_LAUNCH
-  return SVDQ_ERR_UNSUPPORTED_SHAPE;
-}
-
-int svdq_rope_axes_tables(const void* positions, int positions_float, int P, int axes, const int32_t* axis_dims,
-                          const double* axis_theta, int M, int head_dim, void* rope_cos, void* rope_sin,
-                          void* stream) {
-  if (int st = rope_check(positions, P, axes, axis_dims, axis_theta, M, head_dim)) return st;
-  if (head_dim % 2 != 0) return SVDQ_ERR_UNSUPPORTED_SHAPE;
-  if (M == 0) return SVDQ_OK;
-  if (!rope_cos || !rope_sin || !aligned16(rope_cos) || !aligned16(rope_sin)) return SVDQ_ERR_INVALID_ARG;
-  int dev;
-  if (int st = current_device_ok(&dev)) return st;
-  namespace k9 = svdq::k9;
-  const RopeFreqs& rf = rope_freqs(axes, axis_dims, axis_theta, positions_float != 0);
-  const k9::Freqs& fr = rf.fr;
-  k9::TableParams p;
-  p.pos = positions;
-  p.axes = axes;
-  p.P = P;
-  p.M = M;
-  p.pairs = head_dim / 2;
-  p.rot_pairs = rf.rot / 2;
-  p.cos = static_cast<float*>(rope_cos);
-  p.sin = static_cast<float*>(rope_sin);
-  const int bx = (P - 1) / (k9::kTableThreads * k9::kTokens) + 1;
-  // pairs per thread: the fewest that keep the grid within eight blocks per SM
-  const int by = std::max(1, std::min(p.pairs, 8 * sm_count(dev) / bx));
-  p.per = (p.pairs + by - 1) / by;
-  if (!launch_pdl(positions_float ? k9::rope_tables_kernel<true> : k9::rope_tables_kernel<false>, dim3(bx, (p.pairs + p.per - 1) / p.per), k9::kTableThreads, 0, stream, p, fr))
-    return SVDQ_ERR_CUDA;
-  return launch_status();
-}
-
 int svdq_selftest_wait_timeout(void* stream) {
   int dev;
   if (int st = current_device_ok(&dev)) return st;
@@ -1369,3 +865,7 @@ int svdq_device_status(int clear) {
 }
 
 }  // extern "C"
+
+// The calls of the other operators: parts of this translation unit (they use its helpers and the one status word).
+#include "lora_launch.cuh"
+#include "rope_launch.cuh"

@@ -56,3 +56,13 @@ def test_flop_and_byte_counts_of_the_attention_layer():
     # kernel 1: X and U hi|lo in bf16, codes (4 bits), scales (one byte per 16), the smoothing
     # factors and the packed low-rank operand
     assert bench.k1_bytes(M, K) == pytest.approx(33167360.0)
+
+
+def test_operators_beside_the_gemm_are_not_in_its_hashed_sources():
+    """Their launchers were, so that adding one made the GEMM's DRAM capture stale."""
+    import os
+    for name in bench.GEMM_SOURCES:
+        with open(os.path.join(bench.ROOT, "bit_diffusion_transformer_act_b200", "csrc", name)) as f:
+            text = f.read()
+        for word in ("svdq_lora", "qk_norm_rope", "rope_axes_tables", "lora_plan"):
+            assert word not in text, (name, word)
