@@ -301,3 +301,74 @@ def test_partial_slabs_through_a_turning_ring(P, rows):
     off = rows * np.arange(n + 1)
     _check(short(expect), xs, ys, a, b, off, ids, w)
     assert P.svdq_device_status() == 0
+
+
+@pytest.mark.parametrize("case", [
+    (400, 192, 320, 16, 8, 5, [0, 17, 150, 390]),                   # eight slots
+    (300, 128, 192, 96, 1, 3, [0, 130, 150, 300]),                  # three boxes of 32 ranks
+    (300, 128, 192, 48, 2, 3, [0, 130, 150, 300]),                  # three boxes of 16 ranks, twice
+    (260, 64, 64, 16, 7, 3, [0, 240, 260]),                         # 112 ranks in seven slots
+], ids=lambda c: "-".join(str(v) for v in c[:5]))
+def test_ranks_and_slots_of_long_requests(P, case):
+    M, K, N, R, slots, adapters, off = case
+    x, y, a, b = _make(M, K, N, R, slots, adapters, seed=8)
+    ids = _ids(case)
+    ids[0, slots - 1] = -1
+    w = _weights(ids)
+    out = P.svdq_lora_add(x, y, a, b, P.LoraPlan(off, ids, w, M, adapters))
+    _check(out, x, y, a, b, off, ids, w)
+    assert P.svdq_device_status() == 0
+
+
+@pytest.mark.parametrize("off", [[0, 3, 20], [0, 140, 300]])
+def test_other_adapters_of_the_pool_are_not_read_into_a_result(P, off):
+    M, K, N = off[-1], 128, 192
+    x, y, a, b = _make(M, K, N, 48, 1, 3)
+    a[0] = b[0] = a[2] = b[2] = float("nan")
+    ids = np.array([[1], [1]])
+    w = _weights(ids)
+    _check(P.svdq_lora_add(x, y, a, b, P.LoraPlan(off, ids, w, M, 3)), x, y, a[1:2], b[1:2], off, ids * 0, w)
+
+
+def test_a_pool_past_32_bits(P):
+    """The last adapter's B starts beyond 2^31 elements."""
+    adapters, N, K, R, off = 1200, 15360, 64, 128, [0, 5, 40]
+    b = torch.empty((adapters, N, R), dtype=torch.bfloat16, device="cuda")
+    x, y, a1, b1 = _make(off[-1], K, N, R, 1, 1)
+    a = torch.zeros((adapters, R, K), dtype=torch.bfloat16, device="cuda")
+    a[-1], b[-1] = a1[0], b1[0]
+    assert (adapters - 1) * N * R > 2 ** 31
+    w = _weights([[0], [0]])
+    big = P.svdq_lora_add(x, y, a, b, P.LoraPlan(off, [adapters - 1] * 2, w.ravel(), off[-1], adapters))
+    assert torch.equal(big, P.svdq_lora_add(x, y, a1, b1, P.LoraPlan(off, [0, 0], w.ravel(), off[-1], 1)))
+
+
+def test_more_groups_than_a_grid_axis_of_16_bits(P):
+    """A row per request and an adapter per row: 70000 groups, whose parts are formed and added at once."""
+    M, K, N, R = 70000, 64, 64, 16
+    x, y, a, b = _make(M, K, N, R, 1, M)
+    off, ids = np.arange(M + 1), np.arange(M)[::-1].copy()
+    w = _weights(ids)
+    plan = P.LoraPlan(off, ids, w, M, M)
+    assert plan.struct.groups == M
+    out = P.svdq_lora_add(x, y, a, b, plan)
+    pick = np.concatenate([[0, 1, M - 1], np.random.default_rng(0).integers(0, M, 500)])
+    at = torch.from_numpy(pick).cuda()
+    idt = torch.from_numpy(ids[pick]).cuda()
+    _check(out[at], x[at], y[at], a[idt], b[idt], np.arange(len(pick) + 1), np.arange(len(pick))[:, None], w[pick, None])
+
+
+def test_a_workspace_of_the_callers(P):
+    """One workspace serves calls of one stream after another; a short or misplaced one is refused."""
+    M, K, N = 300, 256, 192
+    x, y, a, b = _make(M, K, N, 32, 1, 3)
+    plans = [P.LoraPlan([0, 200, 204], [0, 1], [1.0, 2.0], M, 3), P.LoraPlan(list(range(41)), np.arange(40) % 3, np.ones(40), M, 3)]
+    need = [P.svdq_lora_workspace_bytes(p, K, 32) for p in plans]
+    ws = torch.empty(max(need), dtype=torch.uint8, device="cuda")
+    expect = [P.svdq_lora_add(x, y, a, b, p) for p in plans]
+    got = [P.svdq_lora_add(x, y, a, b, p, workspace=ws) for _ in range(3) for p in plans]
+    assert all(torch.equal(g, expect[i % 2]) for i, g in enumerate(got))
+    with pytest.raises(ValueError, match="workspace"):
+        P.svdq_lora_add(x, y, a, b, plans[0], workspace=ws[:need[0] - 16])
+    with pytest.raises(ValueError, match="workspace"):
+        P.svdq_lora_add(x, y, a, b, plans[0], workspace=ws.cpu())

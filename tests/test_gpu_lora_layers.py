@@ -227,3 +227,22 @@ def test_inductors_cuda_graphs_do_not_keep_a_plan(P):
             plan = plans[i // 4]
             layer.set_plan(plan)
             assert torch.equal(run(x).clone(), P.svdq_lora_add(x, base(x), layer.A, layer.B, plan))
+
+
+def test_operators_that_read_a_plans_sizes_agree_with_their_fakes(P, block):
+    w, base, layer, x, pos, nq, nk = block
+    plan = P.LoraPlan([0, 3, 200, 300], [0, 1, 2], [1.0, 1.0, 1.0], 300, 3)
+    sizes = torch.tensor(plan.sizes())
+    checks = ("test_schema", "test_faketensor", "test_aot_dispatch_dynamic")
+    for op in (torch.ops.svdq.lora_add_planned_, torch.ops.svdq.lora_add):
+        torch.library.opcheck(op.default, (x, base(x), layer.A, layer.B, plan.words, sizes), test_utils=checks)
+    y = base(x)
+    out = torch.ops.svdq.lora_add(x, y, layer.A, layer.B, plan.words, sizes)
+    assert torch.equal(y, base(x))
+    torch.ops.svdq.lora_add_planned_(x, y, layer.A, layer.B, plan.words, sizes)
+    assert torch.equal(y, out) and not torch.equal(y, base(x))
+    with pytest.raises(RuntimeError, match="no gradient"):
+        torch.ops.svdq.lora_add_planned_(x.clone().requires_grad_(), y, layer.A, layer.B, plan.words, sizes)
+    z = torch.ops.svdq.lora_add(x.clone().requires_grad_(), y, layer.A, layer.B, plan.words, sizes)
+    with pytest.raises(RuntimeError, match="no gradient"):
+        z.float().sum().backward()
