@@ -247,7 +247,8 @@ int svdq_lora_add(const void* X, int64_t ldx, const void* Yin, int64_t ldyin, co
     return SVDQ_ERR_UNSUPPORTED_SHAPE;
   // tile coordinates and piece counts are 32-bit
   const int64_t all_tiles = static_cast<int64_t>(plan->tiles) + plan->copy_tiles;
-  if (static_cast<int64_t>(plan->adapters) * N > INT32_MAX - N || all_tiles * (N / 64) > INT32_MAX ||
+  if (static_cast<int64_t>(plan->adapters) * N > INT32_MAX - N ||
+      static_cast<int64_t>(plan->adapters) * rank > INT32_MAX - rank || all_tiles * (N / 64) > INT32_MAX ||
       all_tiles * svdq::kLoraTileRows > INT32_MAX)
     return SVDQ_ERR_UNSUPPORTED_SHAPE;
   if (M == 0) return SVDQ_OK;

@@ -190,3 +190,10 @@ def test_python_wrapper_refuses_before_the_call():
 def test_a_single_row_is_in_place_whatever_its_strides():
     s = _pack([0, 1], [0], [1], M=1)[1]
     assert _add(s, X=ctypes.c_void_p(1 << 24), M=1, ldy=256) == 4
+
+
+def test_pools_whose_rows_pass_32_bits_are_refused():
+    far = ctypes.c_void_p(1 << 24)
+    s = _pack([0, 4, 10], [0, 1], [1, 1], adapters=1 << 24)[1]
+    assert _add(s, X=far, rank=128, N=64, ldyin=64, ldy=64) == 2        # rows of A
+    assert _add(s, X=far, N=128) == 2                                   # rows of B
