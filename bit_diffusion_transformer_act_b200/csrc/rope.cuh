@@ -412,8 +412,10 @@ qk_norm_rope_kernel(const __grid_constant__ Params p, const __grid_constant__ Fr
 // Kernel 10: a thread owns kTokens positions (columns of the tables, kTableThreads apart) and walks over a share of
 // the pairs; 32 neighbouring threads write one 128-byte line of each table.  Tokens m, m + P, m + 2P, ... have the
 // same position and get the same values.  Bound by its stores, 8 bytes per (token, pair), if the instructions are
-// few: 131075 tokens, 64 pairs (floor 10.6 us): 27 us with a 64-bit reduction and the library's sine and cosine,
-// 18.9 us with fixed-point turns and one token per thread (20 of 55 instructions were the loop's), 15.2 us with four.
+// few and its blocks fit at once.  131075 tokens, 64 pairs, float positions (floor 10.6 us): 27 us with a 64-bit
+// reduction and the library's sine and cosine, 18.9 us with fixed-point turns and one token per thread (20 of 55
+// instructions were the loop's), 15.2 us with four.  Float positions take 40 registers, so six blocks fit on an SM
+// where the host asks for eight: the 1032 blocks of this case are a wave of 888 and a rest.
 constexpr int kTokens = 4;
 struct TableParams {
   const void* pos;

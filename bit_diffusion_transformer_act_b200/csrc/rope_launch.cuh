@@ -237,7 +237,8 @@ int svdq_rope_axes_tables(const void* positions, int positions_float, int P, int
   p.cos = static_cast<float*>(rope_cos);
   p.sin = static_cast<float*>(rope_sin);
   const int bx = (P - 1) / (k9::kTableThreads * k9::kTokens) + 1;
-  // pairs per thread: the fewest that keep the grid within eight blocks per SM
+  // pairs per thread: the fewest that keep the grid within eight blocks per SM (integer positions; with float ones
+  // six fit)
   const int by = std::max(1, std::min(p.pairs, 8 * sm_count(dev) / bx));
   p.per = (p.pairs + by - 1) / by;
   if (!launch_pdl(positions_float ? k9::rope_tables_kernel<true> : k9::rope_tables_kernel<false>, dim3(bx, (p.pairs + p.per - 1) / p.per), k9::kTableThreads, 0, stream, p, fr))
